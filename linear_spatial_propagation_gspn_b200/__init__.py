@@ -22,6 +22,7 @@ import os
 import torch
 
 from . import build as _build_mod
+from . import seq as _seq
 
 LIB_PATH = _build_mod.LIB
 
@@ -48,7 +49,7 @@ class GspnError(RuntimeError):
 
 _lib = None
 
-# (name, restype, argtypes) of every symbol include/gspn.h declares.
+# (name, restype, argtypes) of every symbol that include/gspn.h and include/gspn_seq.h declare.
 _VP, _SZ, _I, _U64 = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int, ctypes.c_ulonglong
 _DP = ctypes.POINTER(GspnDesc)
 SIGNATURES = {
@@ -70,6 +71,7 @@ SIGNATURES = {
     "gspn_proxy_forward": (_I, [_DP, _I, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _SZ, _VP]),
     "gspn_status_string": (ctypes.c_char_p, [_I]),
     "gspn_version": (_I, []),
+    **_seq.SIGNATURES,           # include/gspn_seq.h
 }
 
 
@@ -356,3 +358,11 @@ def gspn(x, a, lam, u, wmode: int = PER_CHANNEL, dir_mask: int = DIR_ALL, chunk:
     """Differentiable GSPN propagation (libgspn forward and backward); chunk > 0 = local;
     per_dir = 1: per-direction lam and u (D, N, C, H, W)."""
     return GSPNFunction.apply(x, a, lam, u, wmode, dir_mask, chunk, per_dir)
+
+
+# Token-sequence operators (include/gspn_seq.h).
+conv_forward, conv_backward, conv_step, causal_conv = (
+    _seq.conv_forward, _seq.conv_backward, _seq.conv_step, _seq.causal_conv)
+ssm_forward, ssm_forward_save, ssm_backward, ssm_step, selective_scan = (
+    _seq.ssm_forward, _seq.ssm_forward_save, _seq.ssm_backward, _seq.ssm_step, _seq.selective_scan)
+norm_forward, norm_backward, block_norm = _seq.norm_forward, _seq.norm_backward, _seq.block_norm

@@ -1,0 +1,562 @@
+// k_conv.cu -- short causal convolution over token sequences, one filter of K taps per channel:
+//   u_t = bias + sum_{k<K} w_k x_{t-K+1+k},   y_t = u_t or u_t sigmoid(u_t).
+//
+// A few operations per element, so memory traffic bounds it: x read and y written once. A thread
+// keeps a vector of channels (16 bytes forward) and walks a run of tokens with the K - 1 inputs
+// before the present one in registers, so each input is loaded once per run; the K - 1 tokens that
+// neighbouring runs share come from the caches.
+#include "seq_common.cuh"
+
+namespace gspn {
+namespace seq {
+namespace {
+
+constexpr int kRunFwd = 16;     // tokens of a thread, forward
+constexpr int kRunBwd = 32;     // tokens of a thread, backward
+constexpr int kBatch = 4;       // tokens whose loads are in flight together
+
+struct ConvArgs {
+    int B, L, C, S, silu;
+    bool wide;
+    const void* x;
+    long long x_row, x_tok;
+    const float *w, *bias;
+    const int* cu;
+    const void *state0, *dy, *dstate;
+    void *y, *state, *dx, *dstate0;
+    float* part;
+    int nvec, run, runs;        // channel vectors; tokens of a run; runs of a row
+};
+
+// L consecutive elements (L * sizeof(T) = 8 or 16 bytes when wide), as floats.
+template <typename T, int L>
+__device__ __forceinline__ void ld_ch(const T* p, float (&v)[L], int n, bool wide) {
+    if (wide && n >= L) {
+        ld_lanes<T, L>(p, v);
+    } else {
+#pragma unroll
+        for (int i = 0; i < L; ++i) v[i] = i < n ? Io<T>::ld(p + i) : 0.f;
+    }
+}
+template <typename T, int L>
+__device__ __forceinline__ void st_ch(T* p, const float (&v)[L], int n, bool wide) {
+    if (wide && n >= L) {
+        st_lanes<T, L>(p, v);
+    } else {
+#pragma unroll
+        for (int i = 0; i < L; ++i)
+            if (i < n) Io<T>::st(p + i, v[i]);
+    }
+}
+
+// The sequence of token t and its bounds; q = S and end = L where t lies behind the last one.
+struct Seq {
+    int q, start, end;
+};
+__device__ __forceinline__ int cu_at(const ConvArgs& p, int i) { return min(max(p.cu[i], 0), p.L); }
+__device__ __forceinline__ void enter(const ConvArgs& p, Seq& s, int t) {   // moves on to the sequence of t
+    while (s.q < p.S && t >= cu_at(p, s.q + 1)) ++s.q;
+    s.start = s.q < p.S ? min(cu_at(p, s.q), t) : t;
+    s.end = s.q < p.S ? cu_at(p, s.q + 1) : p.L;
+}
+__device__ __forceinline__ Seq find(const ConvArgs& p, int row, int t) {
+    if (!p.cu) return Seq{row, 0, p.L};
+    int lo = 0, hi = p.S;                        // first q with t < cu[q + 1]
+    while (lo < hi) {
+        const int mid = (lo + hi) / 2;
+        if (t < cu_at(p, mid + 1)) hi = mid;
+        else lo = mid + 1;
+    }
+    Seq s{lo, 0, 0};
+    enter(p, s, t);
+    return s;
+}
+
+// The K - 1 inputs before token t of sequence s.
+template <typename T, int K, int L>
+__device__ __forceinline__ void window(const ConvArgs& p, const T* xr, const Seq& s, int t, int c, int n,
+                                       float (&win)[K][L]) {
+#pragma unroll
+    for (int j = 0; j < K - 1; ++j) {
+        const int at = t - (K - 1) + j;
+#pragma unroll
+        for (int i = 0; i < L; ++i) win[j][i] = 0.f;
+        if (at >= s.start) ld_ch<T, L>(xr + at * p.x_tok, win[j], n, p.wide);
+        else if (p.state0)
+            ld_ch<T, L>((const T*)p.state0 + ((long long)s.q * (K - 1) + (K - 1 + at - s.start)) * p.C + c, win[j], n,
+                        p.wide);
+    }
+}
+
+template <int K, int L>
+__device__ __forceinline__ void load_taps(const ConvArgs& p, int c, int n, float (&w)[K][L], float (&b)[L]) {
+#pragma unroll
+    for (int i = 0; i < L; ++i) {
+#pragma unroll
+        for (int k = 0; k < K; ++k) w[k][i] = i < n ? p.w[(long long)(c + i) * K + k] : 0.f;
+        b[i] = i < n && p.bias ? p.bias[c + i] : 0.f;
+    }
+}
+
+template <typename T, int K>
+__global__ void __launch_bounds__(128) k_conv_fwd(const ConvArgs p) {
+    constexpr int V = Vec<T>::V;
+    const long long id = (long long)blockIdx.x * blockDim.x + threadIdx.x;
+    const int cv = (int)(id % p.nvec);
+    const long long rr = id / p.nvec;
+    const int row = (int)(rr / p.runs);
+    if (row >= p.B) return;
+    int t = (int)(rr % p.runs) * p.run;
+    const int te = min(t + p.run, p.L);
+    const int c = cv * V, n = p.C - c;
+    if (p.cu) t = max(t, cu_at(p, 0));
+    if (t >= te) return;
+    float w[K][V], b[V], win[K][V];
+    load_taps<K, V>(p, c, n, w, b);
+    const T* xr = (const T*)p.x + row * p.x_row + c;
+    T* yr = (T*)p.y + (long long)row * p.L * p.C + c;
+    Seq s = find(p, row, t);
+    window<T, K, V>(p, xr, s, t, c, n, win);
+    for (; t < te; t += kBatch) {
+        uint4 raw[kBatch];
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u)
+            raw[u] = t + u < te ? ld_raw<T>(xr + (t + u) * p.x_tok, n, p.wide) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+            if (t + u >= te) break;
+            if (p.cu && t + u >= s.end) {
+                enter(p, s, t + u);
+                window<T, K, V>(p, xr, s, t + u, c, n, win);
+            }
+            if (p.cu && s.q >= p.S) return;                       // behind the last sequence
+            unpack_raw<T>(raw[u], win[K - 1]);
+            float o[V];
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                float a = b[i];
+#pragma unroll
+                for (int k = 0; k < K; ++k) a = fmaf(w[k][i], win[k][i], a);
+                o[i] = p.silu ? silu(a) : a;
+#pragma unroll
+                for (int k = 0; k < K - 1; ++k) win[k][i] = win[k + 1][i];
+            }
+            st_vec<T>(yr + (long long)(t + u) * p.C, o, n, p.wide);
+        }
+    }
+}
+
+// The last K - 1 inputs of every sequence. Thread = (sequence, channel); it reads all of its channel's
+// rows before it writes them, so state may be state0.
+template <typename T, int K>
+__global__ void k_conv_state(const ConvArgs p) {
+    const long long id = (long long)blockIdx.x * blockDim.x + threadIdx.x;
+    const int c = (int)(id % p.C);
+    const long long q = id / p.C;
+    if (q >= p.S) return;
+    const Span sp = span_of(p.cu, (int)q, p.L);
+    T v[K - 1];
+#pragma unroll
+    for (int j = 0; j < K - 1; ++j) {
+        const int at = sp.len - (K - 1) + j;
+        if (at >= 0) v[j] = ((const T*)p.x)[sp.row * p.x_row + (sp.first + at) * p.x_tok + c];
+        else if (p.state0) v[j] = ((const T*)p.state0)[(q * (K - 1) + K - 1 + at) * p.C + c];
+        else v[j] = T(0.f);
+    }
+#pragma unroll
+    for (int j = 0; j < K - 1; ++j) ((T*)p.state)[(q * (K - 1) + j) * p.C + c] = v[j];
+}
+
+// ------------------------------------------------------------------------------------ backward
+//   du_t = dy_t (slope of silu at u_t);  dx_t = sum_k w_k du_{t+K-1-k};  dw_k = sum_t du_t x_{t-K+1+k}
+// A thread walks a run forward, forming u_t again from the inputs, with the K sums of dx that du_t
+// adds to in registers: after token t the one of t - K + 1 is complete. It goes K - 1 tokens past
+// its run for its last sums. A block is 32 channel vectors (4 channels) x 4 runs; it takes several
+// runs in turn and keeps its sums of dw and dbias until the end; k_conv_sum adds the blocks in order.
+constexpr int kVB = 4, kRows = 4;
+
+template <typename T, int K>
+__global__ void __launch_bounds__(128) k_conv_bwd(const ConvArgs p) {
+    __shared__ float red[kRows][K + 1][32 * kVB];
+    const int lane = threadIdx.x & 31, grp = threadIdx.x >> 5;
+    const int c = (blockIdx.x * 32 + lane) * kVB, n = p.C - c;
+    float w[K][kVB], b[kVB], dw[K][kVB], db[kVB];
+#pragma unroll
+    for (int i = 0; i < kVB; ++i) {
+        db[i] = 0.f;
+#pragma unroll
+        for (int k = 0; k < K; ++k) dw[k][i] = 0.f;
+    }
+    if (n > 0) {
+        load_taps<K, kVB>(p, c, n, w, b);
+        const long long all = (long long)p.B * p.runs;
+        for (long long rr = (long long)blockIdx.y * kRows + grp; rr < all; rr += (long long)gridDim.y * kRows) {
+            const int row = (int)(rr / p.runs);
+            int ta = (int)(rr % p.runs) * p.run;
+            const int tb = min(ta + p.run, p.L);
+            if (p.cu) ta = max(ta, cu_at(p, 0));
+            if (ta >= tb) continue;
+            const T* xr = (const T*)p.x + row * p.x_row + c;
+            const T* gr = (const T*)p.dy + (long long)row * p.L * p.C + c;
+            T* dr = (T*)p.dx + (long long)row * p.L * p.C + c;
+            Seq s = find(p, row, ta);
+            if (p.cu && s.q >= p.S) continue;
+            float win[K][kVB], acc[K][kVB], run_dw[K][kVB], run_db[kVB];
+            window<T, K, kVB>(p, xr, s, ta, c, n, win);
+#pragma unroll
+            for (int i = 0; i < kVB; ++i) {
+                run_db[i] = 0.f;
+#pragma unroll
+                for (int k = 0; k < K; ++k) acc[k][i] = run_dw[k][i] = 0.f;
+            }
+            // writes token `at`'s sum, held in v, if the run owns it
+            auto put = [&](int at, float (&v)[kVB]) {
+                if (at < ta || at < s.start || at >= tb) return;
+                const int m = at - s.end + K - 1;                 // its row in the state behind the sequence
+                if (m >= 0 && p.dstate) {
+                    float d[kVB];
+                    ld_ch<T, kVB>((const T*)p.dstate + ((long long)s.q * (K - 1) + m) * p.C + c, d, n, p.wide);
+#pragma unroll
+                    for (int i = 0; i < kVB; ++i) v[i] += d[i];
+                }
+                st_ch<T, kVB>(dr + (long long)at * p.C, v, n, p.wide);
+            };
+            const int stop = min(tb + K - 1, p.L);
+            int t = ta;
+            bool open = true;
+            for (; open && t < stop; t += kBatch) {
+                float xs[kBatch][kVB], gs[kBatch][kVB];
+#pragma unroll
+                for (int u = 0; u < kBatch; ++u) {
+                    const bool in = t + u < stop;
+                    ld_ch<T, kVB>(xr + (in ? (t + u) * p.x_tok : 0), xs[u], in ? n : 0, p.wide);
+                    ld_ch<T, kVB>(gr + (in ? (long long)(t + u) * p.C : 0), gs[u], in ? n : 0, p.wide);
+                }
+#pragma unroll
+                for (int u = 0; u < kBatch; ++u) {
+                    const int tt = t + u;
+                    if (!open || tt >= stop) break;
+                    if (tt >= s.end) {                            // the sequence is over: its last sums are complete
+#pragma unroll
+                        for (int k = 0; k < K - 1; ++k) put(tt - (K - 1) + k, acc[k]);
+                        open = tt < tb;
+                        if (open) {
+                            enter(p, s, tt);
+                            open = s.q < p.S;
+                        }
+                        if (!open) break;
+                        window<T, K, kVB>(p, xr, s, tt, c, n, win);
+#pragma unroll
+                        for (int k = 0; k < K; ++k)
+#pragma unroll
+                            for (int i = 0; i < kVB; ++i) acc[k][i] = 0.f;
+                    }
+#pragma unroll
+                    for (int i = 0; i < kVB; ++i) {
+                        win[K - 1][i] = xs[u][i];
+                        float du = gs[u][i];
+                        if (p.silu) {
+                            float a = b[i];
+#pragma unroll
+                            for (int k = 0; k < K; ++k) a = fmaf(w[k][i], win[k][i], a);
+                            du *= silu_slope(a);
+                        }
+#pragma unroll
+                        for (int k = 0; k < K; ++k) acc[k][i] = fmaf(w[k][i], du, acc[k][i]);
+                        if (tt < tb) {
+                            run_db[i] += du;
+#pragma unroll
+                            for (int k = 0; k < K; ++k) run_dw[k][i] = fmaf(du, win[k][i], run_dw[k][i]);
+                        }
+                    }
+                    put(tt - (K - 1), acc[0]);
+#pragma unroll
+                    for (int i = 0; i < kVB; ++i) {
+#pragma unroll
+                        for (int k = 0; k < K - 1; ++k) {
+                            acc[k][i] = acc[k + 1][i];
+                            win[k][i] = win[k + 1][i];
+                        }
+                        acc[K - 1][i] = 0.f;
+                    }
+                }
+            }
+            if (open && stop == s.end) {                          // ended with the sequence, inside the loop's last batch
+#pragma unroll
+                for (int k = 0; k < K - 1; ++k) put(stop - (K - 1) + k, acc[k]);
+            }
+#pragma unroll
+            for (int i = 0; i < kVB; ++i) {
+                db[i] += run_db[i];
+#pragma unroll
+                for (int k = 0; k < K; ++k) dw[k][i] += run_dw[k][i];
+            }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < kVB; ++i) {
+#pragma unroll
+        for (int k = 0; k < K; ++k) red[grp][k][lane * kVB + i] = dw[k][i];
+        red[grp][K][lane * kVB + i] = db[i];
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < (K + 1) * 32 * kVB; e += blockDim.x) {
+        const int k = e / (32 * kVB), cc = e % (32 * kVB);
+        float v = 0.f;
+#pragma unroll
+        for (int g = 0; g < kRows; ++g) v += red[g][k][cc];
+        const int ch = blockIdx.x * 32 * kVB + cc;
+        if (ch < p.C) p.part[((long long)blockIdx.y * (K + 1) + k) * p.C + ch] = v;
+    }
+}
+
+// dw and dbias: the blocks' sums in order. Thread = (tap or bias, channel).
+__global__ void k_conv_sum(const float* part, int blocks, int C, int K, float* dw, float* dbias) {
+    const int i = blockIdx.x * blockDim.x + threadIdx.x;
+    if (i >= (K + 1) * C) return;
+    const int k = i / C, c = i % C;
+    float v = 0.f;
+    for (int g = 0; g < blocks; ++g) v += part[((long long)g * (K + 1) + k) * C + c];
+    if (k < K) dw[(long long)c * K + k] = v;
+    else if (dbias) dbias[c] = v;
+}
+
+// Gradient of state0: state row j stands K-1-j places before the sequence and meets u_i, i <= j,
+// through tap j - i; rows that are still in the state behind a short sequence take dstate as well.
+// Thread = (sequence, channel).
+template <typename T, int K>
+__global__ void k_conv_dstate(const ConvArgs p) {
+    const long long id = (long long)blockIdx.x * blockDim.x + threadIdx.x;
+    const int c = (int)(id % p.C);
+    const long long q = id / p.C;
+    if (q >= p.S) return;
+    const Span sp = span_of(p.cu, (int)q, p.L);
+    const T* xr = (const T*)p.x + sp.row * p.x_row + c;
+    float w[K], line[2 * (K - 1)], out[K - 1];
+#pragma unroll
+    for (int k = 0; k < K; ++k) w[k] = p.w[(long long)c * K + k];
+#pragma unroll
+    for (int j = 0; j < K - 1; ++j) {
+        line[j] = Io<T>::ld((const T*)p.state0 + (q * (K - 1) + j) * p.C + c);
+        line[K - 1 + j] = j < sp.len ? Io<T>::ld(xr + (sp.first + j) * p.x_tok) : 0.f;
+        out[j] = 0.f;
+        const int m = j - sp.len;
+        if (p.dstate && m >= 0) out[j] = Io<T>::ld((const T*)p.dstate + (q * (K - 1) + m) * p.C + c);
+    }
+#pragma unroll
+    for (int i = 0; i < K - 1; ++i) {
+        if (i < sp.len) {
+            float du = Io<T>::ld((const T*)p.dy + ((long long)sp.row * p.L + sp.first + i) * p.C + c);
+            if (p.silu) {
+                float a = p.bias ? p.bias[c] : 0.f;
+#pragma unroll
+                for (int k = 0; k < K; ++k) a = fmaf(w[k], line[i + k], a);
+                du *= silu_slope(a);
+            }
+#pragma unroll
+            for (int j = i; j < K - 1; ++j) out[j] = fmaf(w[j - i], du, out[j]);
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < K - 1; ++j) Io<T>::st((T*)p.dstate0 + (q * (K - 1) + j) * p.C + c, out[j]);
+}
+
+// ----------------------------------------------------------------------------------- one token
+// Thread = a vector of channels of one row. Rows that name the slot of an earlier row leave their
+// token to that row, which takes them in order.
+template <typename T, int K>
+__global__ void __launch_bounds__(128) k_conv_step(const ConvArgs p, const int* idx, int slots) {
+    constexpr int V = Vec<T>::V;
+    const int b0 = blockIdx.y;
+    const int slot = idx ? idx[b0] : b0;
+    if (slot < 0 || slot >= slots) return;
+    int more = 0;
+    if (idx) {
+        bool earlier = false, later = false;
+        for (int b = threadIdx.x; b < p.B; b += blockDim.x) {
+            const bool same = b != b0 && idx[b] == slot;
+            earlier |= same && b < b0;
+            later |= same && b > b0;
+        }
+        if (__syncthreads_or(earlier)) return;
+        more = __syncthreads_or(later);
+    }
+    const int c = (blockIdx.x * blockDim.x + threadIdx.x) * V, n = p.C - c;
+    if (n <= 0) return;
+    T* st = (T*)p.state + (long long)slot * (K - 1) * p.C + c;
+    float win[K][V], w[K][V], bias[V];
+#pragma unroll
+    for (int j = 0; j < K - 1; ++j) ld_ch<T, V>(st + (long long)j * p.C, win[j], n, p.wide);
+    load_taps<K, V>(p, c, n, w, bias);
+    for (int b = b0; b < (more ? p.B : b0 + 1); ++b) {
+        if (b != b0 && idx[b] != slot) continue;
+        ld_ch<T, V>((const T*)p.x + b * p.x_row + c, win[K - 1], n, p.wide);
+        float o[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            float a = bias[i];
+#pragma unroll
+            for (int k = 0; k < K; ++k) a = fmaf(w[k][i], win[k][i], a);
+            o[i] = p.silu ? silu(a) : a;
+#pragma unroll
+            for (int k = 0; k < K - 1; ++k) win[k][i] = win[k + 1][i];
+        }
+        st_ch<T, V>((T*)p.y + (long long)b * p.C + c, o, n, p.wide);
+    }
+#pragma unroll
+    for (int j = 0; j < K - 1; ++j) st_ch<T, V>(st + (long long)j * p.C, win[j], n, p.wide);
+}
+
+// ---------------------------------------------------------------------------------------- host
+bool make_args(const gspn_conv_desc* d, ConvArgs* p) {
+    if (!d) return false;
+    if (d->B < 1 || d->L < 0 || d->C < 1 || d->K < 2 || d->K > 4 || d->S < 0 || !dtype_ok(d->dtype)) return false;
+    if (d->silu != 0 && d->silu != 1) return false;
+    if (d->S > 0 && d->B != 1) return false;
+    if (d->x_row < 0 || d->x_tok < 0) return false;
+    *p = ConvArgs{};
+    p->B = d->B; p->L = d->L; p->C = d->C; p->silu = d->silu;
+    p->S = d->S > 0 ? d->S : d->B;
+    p->x_row = d->x_row; p->x_tok = d->x_tok;
+    return true;
+}
+bool fits(const gspn_conv_desc& d) {
+    const long long seqs = d.S > 0 ? d.S : d.B;
+    return d.L <= (1 << 30) && (long long)d.B * d.L <= (1LL << 31) - 1 && (long long)d.C * (d.K + 1) < (1LL << 30) &&
+           (long long)d.B * d.L / 4 * d.C < (1LL << 36) && seqs * d.C < (1LL << 36);
+}
+// Blocks along the tokens of the backward pass: enough to fill the SMs eight times, no more than there
+// are groups of runs.
+int bwd_blocks(const gspn_conv_desc& d) {
+    const long long gx = (d.C + 32 * kVB - 1) / (32 * kVB);
+    const long long groups = ((long long)d.B * ((d.L + kRunBwd - 1) / kRunBwd) + kRows - 1) / kRows;
+    long long gy = (8LL * device_sm_count() + gx - 1) / gx;
+    gy = gy < groups ? gy : groups;
+    gy = gy < 65535 ? gy : 65535;
+    return gy > 0 ? (int)gy : 1;
+}
+
+template <typename F>
+void with_taps(int dtype, int K, F&& f) {
+    auto by = [&](auto t) {
+        if (K == 2) f(t, std::integral_constant<int, 2>());
+        else if (K == 3) f(t, std::integral_constant<int, 3>());
+        else f(t, std::integral_constant<int, 4>());
+    };
+    if (dtype == GSPN_F32) by(float{});
+    else by(__nv_bfloat16{});
+}
+
+}  // namespace
+}  // namespace seq
+}  // namespace gspn
+
+using namespace gspn;
+using namespace gspn::seq;
+
+extern "C" {
+
+size_t gspn_conv_workspace_size(const gspn_conv_desc* desc, int for_backward) {
+    ConvArgs p;
+    if (!make_args(desc, &p) || !fits(*desc)) return 0;
+    if (!for_backward) return 256;
+    return 256 + align256((size_t)bwd_blocks(*desc) * (desc->K + 1) * desc->C * sizeof(float));
+}
+
+gspn_status gspn_conv_forward(const gspn_conv_desc* desc, const void* x, const float* w, const float* bias,
+                              const int* cu, const void* state0, void* y, void* state, void* stream) {
+    ConvArgs p;
+    if (!make_args(desc, &p)) return GSPN_ERR_INVALID_ARG;
+    if ((desc->S > 0) != (cu != nullptr) || !w || (p.L > 0 && (!x || !y))) return GSPN_ERR_INVALID_ARG;
+    if (!fits(*desc)) return GSPN_ERR_UNSUPPORTED;
+    const size_t es = dtype_size(desc->dtype);
+    for (const void* q : {x, state0, (const void*)y, (const void*)state})
+        if (!aligned_to(q, es)) return GSPN_ERR_ALIGNMENT;
+    for (const void* q : {(const void*)w, (const void*)bias, (const void*)cu})
+        if (!aligned_to(q, 4)) return GSPN_ERR_ALIGNMENT;
+    p.x = x; p.w = w; p.bias = bias; p.cu = cu; p.state0 = state0; p.y = y; p.state = state;
+    p.wide = (p.C * es) % 16 == 0 && wide_ok(x, p.x_row, p.x_tok, es) && aligned_to(y, 16) && aligned_to(state0, 16);
+    const int V = desc->dtype == GSPN_F32 ? 4 : 8;
+    p.nvec = (p.C + V - 1) / V;
+    // Short inputs are cut into runs of kBatch tokens, so that more threads share them.
+    const long long threads16 = (long long)p.B * ((p.L + kRunFwd - 1) / kRunFwd) * p.nvec;
+    p.run = threads16 >= 1024LL * device_sm_count() ? kRunFwd : kBatch;
+    p.runs = (p.L + p.run - 1) / p.run;
+    const long long total = (long long)p.B * p.runs * p.nvec;
+    cudaStream_t st = (cudaStream_t)stream;
+    with_taps(desc->dtype, desc->K, [&](auto t, auto k) {
+        using T = decltype(t);
+        constexpr int K = decltype(k)::value;
+        if (total > 0) k_conv_fwd<T, K><<<(unsigned)((total + 127) / 128), 128, 0, st>>>(p);
+        if (state) {
+            const long long n = (long long)p.S * p.C;
+            k_conv_state<T, K><<<(unsigned)((n + 127) / 128), 128, 0, st>>>(p);
+        }
+    });
+    return last_status();
+}
+
+gspn_status gspn_conv_backward(const gspn_conv_desc* desc, const void* x, const float* w, const float* bias,
+                               const int* cu, const void* state0, const void* dy, const void* dstate, void* dx,
+                               float* dw, float* dbias, void* dstate0, void* ws, size_t ws_bytes, void* stream) {
+    ConvArgs p;
+    if (!make_args(desc, &p)) return GSPN_ERR_INVALID_ARG;
+    if ((desc->S > 0) != (cu != nullptr) || !w || !dw || !ws) return GSPN_ERR_INVALID_ARG;
+    if (p.L > 0 && (!x || !dy || !dx)) return GSPN_ERR_INVALID_ARG;
+    if (dstate0 && !state0) return GSPN_ERR_INVALID_ARG;
+    if (!fits(*desc)) return GSPN_ERR_UNSUPPORTED;
+    const size_t es = dtype_size(desc->dtype);
+    for (const void* q : {x, state0, dy, dstate, (const void*)dx, (const void*)dstate0})
+        if (!aligned_to(q, es)) return GSPN_ERR_ALIGNMENT;
+    for (const void* q : {(const void*)w, (const void*)bias, (const void*)cu, (const void*)dw, (const void*)dbias})
+        if (!aligned_to(q, 4)) return GSPN_ERR_ALIGNMENT;
+    if (!aligned_to(ws, 16)) return GSPN_ERR_ALIGNMENT;
+    if (ws_bytes < gspn_conv_workspace_size(desc, 1)) return GSPN_ERR_WORKSPACE;
+    p.x = x; p.w = w; p.bias = bias; p.cu = cu; p.state0 = state0; p.dy = dy; p.dstate = dstate; p.dx = dx;
+    p.dstate0 = dstate0;
+    p.part = (float*)((char*)ws + 256);
+    p.wide = (p.C * es) % 16 == 0 && wide_ok(x, p.x_row, p.x_tok, es) && aligned_to(dy, 16) && aligned_to(dx, 16) &&
+             aligned_to(state0, 16) && aligned_to(dstate, 16);
+    p.run = kRunBwd;
+    p.runs = (p.L + kRunBwd - 1) / kRunBwd;
+    const int gy = bwd_blocks(*desc);
+    cudaStream_t st = (cudaStream_t)stream;
+    with_taps(desc->dtype, desc->K, [&](auto t, auto k) {
+        using T = decltype(t);
+        constexpr int K = decltype(k)::value;
+        const dim3 grid((p.C + 32 * kVB - 1) / (32 * kVB), gy);
+        k_conv_bwd<T, K><<<grid, 128, 0, st>>>(p);
+        k_conv_sum<<<((K + 1) * p.C + 127) / 128, 128, 0, st>>>(p.part, gy, p.C, K, dw, dbias);
+        if (dstate0) {
+            const long long n = (long long)p.S * p.C;
+            k_conv_dstate<T, K><<<(unsigned)((n + 127) / 128), 128, 0, st>>>(p);
+        }
+    });
+    return last_status();
+}
+
+gspn_status gspn_conv_step(const gspn_conv_desc* desc, const void* x, const float* w, const float* bias,
+                           const int* idx, int slots, void* state, void* y, void* stream) {
+    ConvArgs p;
+    if (!make_args(desc, &p) || desc->L != 1 || desc->S != 0 || slots < 1) return GSPN_ERR_INVALID_ARG;
+    if (!x || !w || !state || !y || (!idx && slots < p.B)) return GSPN_ERR_INVALID_ARG;
+    if (!fits(*desc) || p.B > 65535) return GSPN_ERR_UNSUPPORTED;
+    const size_t es = dtype_size(desc->dtype);
+    for (const void* q : {x, (const void*)state, (const void*)y})
+        if (!aligned_to(q, es)) return GSPN_ERR_ALIGNMENT;
+    for (const void* q : {(const void*)w, (const void*)bias, (const void*)idx})
+        if (!aligned_to(q, 4)) return GSPN_ERR_ALIGNMENT;
+    p.x = x; p.w = w; p.bias = bias; p.y = y; p.state = state;
+    p.wide = (p.C * es) % 16 == 0 && wide_ok(x, p.x_row, 0, es) && aligned_to(y, 16) && aligned_to(state, 16);
+    const int V = desc->dtype == GSPN_F32 ? 4 : 8;
+    const int nvec = (p.C + V - 1) / V;
+    cudaStream_t st = (cudaStream_t)stream;
+    with_taps(desc->dtype, desc->K, [&](auto t, auto k) {
+        using T = decltype(t);
+        constexpr int K = decltype(k)::value;
+        k_conv_step<T, K><<<dim3((nvec + 127) / 128, p.B), 128, 0, st>>>(p, idx, slots);
+    });
+    return last_status();
+}
+
+}  // extern "C"

@@ -1,0 +1,105 @@
+// seq_common.cuh -- device helpers of the token-sequence operators (convolution, selective scan,
+// norms around a block).
+#pragma once
+
+#include "gspn_common.cuh"
+#include "gspn_internal.h"
+#include "gspn_seq.h"
+
+namespace gspn {
+namespace seq {
+
+// ------------------------------------------------------------------ vectors of 16 bytes
+// V consecutive elements (8 bf16 or 4 fp32). `n` of them exist; the rest read as zero and are not
+// written. `wide` (uniform) says that whole vectors are 16-byte aligned: otherwise, and at a ragged
+// end, elements go one by one.
+template <typename T> struct Vec { static constexpr int V = 16 / sizeof(T); };
+
+template <typename T>
+__device__ __forceinline__ uint4 ld_raw(const T* p, int n, bool wide) {
+    constexpr int V = Vec<T>::V;
+    if (wide && n >= V) return *(const uint4*)p;
+    uint4 q = make_uint4(0, 0, 0, 0);
+    if constexpr (sizeof(T) == 4) {
+        const uint32_t* s = (const uint32_t*)p;
+        if (n > 0) q.x = s[0];
+        if (n > 1) q.y = s[1];
+        if (n > 2) q.z = s[2];
+        if (n > 3) q.w = s[3];
+    } else {
+        const uint16_t* s = (const uint16_t*)p;
+        auto two = [&](int i) { return (n > i ? (uint32_t)s[i] : 0u) | (n > i + 1 ? (uint32_t)s[i + 1] << 16 : 0u); };
+        q.x = two(0); q.y = two(2); q.z = two(4); q.w = two(6);
+    }
+    return q;
+}
+
+template <typename T>
+__device__ __forceinline__ void unpack_raw(const uint4& q, float (&v)[Vec<T>::V]) {
+    if constexpr (sizeof(T) == 4) {
+        v[0] = __uint_as_float(q.x); v[1] = __uint_as_float(q.y);
+        v[2] = __uint_as_float(q.z); v[3] = __uint_as_float(q.w);
+    } else {
+        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            v[2 * k] = __uint_as_float(w[k] << 16);          // bf16 is the upper half of an fp32
+            v[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
+        }
+    }
+}
+
+template <typename T>
+__device__ __forceinline__ void st_vec(T* p, const float (&v)[Vec<T>::V], int n, bool wide) {
+    constexpr int V = Vec<T>::V;
+    if (wide && n >= V) {
+        st_lanes<T, V>(p, v);
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (i < n) Io<T>::st(p + i, v[i]);
+    }
+}
+
+// ------------------------------------------------------------------ functions
+__device__ __forceinline__ float ex2(float v) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+__device__ __forceinline__ float sigmoid(float v) { return __fdividef(1.f, 1.f + __expf(-v)); }
+// exp(-v) may overflow to infinity, where the quotient is the right 0.
+__device__ __forceinline__ float silu(float v) { return __fdividef(v, 1.f + __expf(-v)); }
+// d/dv silu = s + v s (1 - s)
+__device__ __forceinline__ float silu_slope(float v) {
+    const float s = sigmoid(v);
+    return fmaf(v * s, 1.f - s, s);
+}
+
+// ------------------------------------------------------------------ sequences
+// Where sequence q lies: its row, first token and length. Entries of cu are clamped to the row, so
+// no value of them leads out of bounds.
+struct Span {
+    int row, first, len;
+};
+__device__ __forceinline__ Span span_of(const int* cu, int q, int L) {
+    if (!cu) return Span{q, 0, L};
+    const int a = min(max(cu[q], 0), L), b = min(max(cu[q + 1], a), L);
+    return Span{0, a, b - a};
+}
+
+inline bool aligned_to(const void* p, size_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
+inline size_t dtype_size(int dtype) { return dtype == GSPN_F32 ? 4 : 2; }
+inline bool dtype_ok(int dtype) { return dtype == GSPN_F32 || dtype == GSPN_BF16; }
+// True where every vector of an input with these strides is 16-byte aligned.
+inline bool wide_ok(const void* p, long long row, long long tok, size_t es) {
+    return aligned_to(p, 16) && (row * (long long)es) % 16 == 0 && (tok * (long long)es) % 16 == 0;
+}
+inline gspn_status last_status() { return cudaGetLastError() == cudaSuccess ? GSPN_OK : GSPN_ERR_CUDA; }
+
+}  // namespace seq
+}  // namespace gspn

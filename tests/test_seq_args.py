@@ -1,0 +1,182 @@
+"""Host-side checks of the token-sequence calls (no GPU needed): what they refuse is refused before
+anything is launched. Pointers are made up; no call here gets past its checks."""
+import ctypes
+
+import pytest
+import torch
+
+import linear_spatial_propagation_gspn_b200 as g
+from linear_spatial_propagation_gspn_b200 import seq
+
+P = 0x10000
+
+
+def conv(**kw):
+    return seq.ConvDesc(*{**dict(B=2, L=8, C=16, K=4, S=0, dtype=0, silu=1, x_row=128, x_tok=16), **kw}.values())
+
+
+def ssm(**kw):
+    base = dict(B=2, L=8, C=16, G=1, N=16, S=0, dtype=0, softplus=1, x_row=128, x_tok=16, dt_row=128, dt_tok=16, z_row=128, z_tok=16,
+                b_row=128, b_tok=16, c_row=128, c_tok=16)
+    return seq.SsmDesc(*{**base, **kw}.values())
+
+
+def norm(**kw):
+    return seq.NormDesc(*{**dict(rows=4, C=16, dtype=0, res_dtype=0, center=0, eps=1e-5, y_row=16, gate_row=16, r_row=16), **kw}.values())
+
+
+def call(name, d, args):
+    return getattr(g.lib(), name)(ctypes.byref(d), *args)
+
+
+# every call with made-up pointers; the positions of the ones that may not be null
+CALLS = {
+    "gspn_conv_forward": (conv, [P, P, P, None, P, P, P, None], (0, 1, 5)),
+    "gspn_conv_backward": (conv, [P, P, P, None, P, P, P, P, P, P, P, P, 1 << 20, None], (0, 1, 5, 7, 8, 11)),
+    "gspn_conv_step": (lambda **k: conv(**{**dict(L=1), **k}), [P, P, P, P, 4, P, P, None], (0, 1, 5, 6)),
+    "gspn_ssm_forward": (ssm, [P, P, P, P, P, P, P, P, None, P, P, P, P, P, 1 << 20, None], (0, 1, 2, 3, 4, 10)),
+    "gspn_ssm_backward": (ssm, [P, P, P, P, P, P, P, P, None, P, P, P, P, P, P, P, P, P, P, P, P, P, 1 << 24, None],
+                          (0, 1, 2, 3, 4, 9, 10, 12, 13, 14, 15, 16, 18, 21)),
+    "gspn_ssm_step": (lambda **k: ssm(**{**dict(L=1), **k}), [P, P, P, P, P, P, P, P, P, 4, P, P, None], (0, 1, 2, 3, 4, 10, 11)),
+    "gspn_norm_forward": (norm, [P, P, P, P, P, P, P, P, P, P, None], (0, 8)),
+    "gspn_norm_backward": (norm, [P] * 18 + [1 << 24, None], (0, 9, 17)),
+}
+BAD = {
+    conv: [dict(B=0), dict(L=-1), dict(C=0), dict(K=1), dict(K=5), dict(S=-1), dict(S=3), dict(dtype=2), dict(silu=2), dict(x_tok=-1)],
+    ssm: [dict(B=0), dict(L=-1), dict(C=0), dict(G=0), dict(G=3), dict(N=0), dict(S=-1), dict(S=2), dict(dtype=2), dict(softplus=3),
+          dict(b_tok=-16)],
+    norm: [dict(rows=-1), dict(C=0), dict(dtype=5), dict(dtype=0, res_dtype=1), dict(center=2), dict(eps=-1.0), dict(eps=float("nan")),
+           dict(r_row=-1)],
+}
+
+
+@pytest.mark.parametrize("name", list(CALLS))
+def test_bad_descriptors(name):
+    make, args, _ = CALLS[name]
+    kind = {"conv": conv, "ssm_": ssm, "norm": norm}[name[5:9]]
+    for bad in BAD[kind]:
+        d = make(**bad)
+        assert call(name, d, args) == g.GSPN_ERR_INVALID_ARG, (name, bad)
+        assert getattr(g.lib(), name.rsplit("_", 1)[0] + "_workspace_size")(ctypes.byref(d), 1) == 0, (name, bad)
+
+
+@pytest.mark.parametrize("name", list(CALLS))
+def test_null_and_misaligned(name):
+    make, args, needed = CALLS[name]
+    for i in needed:
+        a = list(args)
+        a[i] = None
+        assert call(name, make(), a) == g.GSPN_ERR_INVALID_ARG, (name, i)
+    for i, v in enumerate(args[:-1]):
+        if v == P:
+            a = list(args)
+            a[i] = P + 2
+            assert call(name, make(), a) == g.GSPN_ERR_ALIGNMENT, (name, i)
+
+
+def test_optional_parts_that_go_together():
+    make, args, _ = CALLS["gspn_ssm_backward"]
+    a = list(args)
+    a[18] = None                                                    # dz without its place
+    assert call("gspn_ssm_backward", make(), a) == g.GSPN_ERR_INVALID_ARG
+    a = list(args)
+    a[6] = None                                                     # dz, but no z
+    assert call("gspn_ssm_backward", make(), a) == g.GSPN_ERR_INVALID_ARG
+    for name in ("gspn_conv_forward", "gspn_ssm_forward"):          # cu goes with S
+        make, args, _ = CALLS[name]
+        a = list(args)
+        a[3 if "conv" in name else 8] = P
+        assert call(name, make(), a) == g.GSPN_ERR_INVALID_ARG
+        assert call(name, make(B=1, S=2), args) == g.GSPN_ERR_INVALID_ARG
+    make, args, _ = CALLS["gspn_norm_forward"]
+    for i in (2, 6, 9):                                             # b_post without w_post; w_pre and o
+        a = list(args)
+        a[i] = None
+        assert call("gspn_norm_forward", make(), a) == g.GSPN_ERR_INVALID_ARG, i
+    make, args, _ = CALLS["gspn_norm_backward"]
+    for i in (1, 2, 4, 5, 6, 8):
+        a = list(args)
+        a[i] = None
+        assert call("gspn_norm_backward", make(), a) == g.GSPN_ERR_INVALID_ARG, i
+
+
+def test_workspaces():
+    L = g.lib()
+    for name, make, i in (("conv", conv, 12), ("ssm", ssm, 22), ("norm", norm, 18)):
+        d = make()
+        n = getattr(L, f"gspn_{name}_workspace_size")(ctypes.byref(d), 1)
+        assert n > 256
+        _, args, _ = CALLS[f"gspn_{name}_backward"]
+        a = list(args)
+        a[i] = n - 1
+        assert call(f"gspn_{name}_backward", d, a) == g.GSPN_ERR_WORKSPACE
+    d = ssm(B=1, L=100000, C=32)                                    # cut into pieces: the forward pass needs one too
+    n = L.gspn_ssm_workspace_size(ctypes.byref(d), 0)
+    assert n > 256
+    a = list(CALLS["gspn_ssm_forward"][1])
+    a[14] = n - 1
+    assert call("gspn_ssm_forward", d, a) == g.GSPN_ERR_WORKSPACE
+    a[13] = None
+    assert call("gspn_ssm_forward", d, a) == g.GSPN_ERR_INVALID_ARG
+
+
+def test_what_is_too_large():
+    assert call("gspn_ssm_forward", ssm(N=65), CALLS["gspn_ssm_forward"][1]) == g.GSPN_ERR_UNSUPPORTED
+    assert call("gspn_ssm_step", ssm(L=1, N=65), CALLS["gspn_ssm_step"][1]) == g.GSPN_ERR_UNSUPPORTED
+    assert call("gspn_ssm_forward", ssm(B=4, L=1 << 29), CALLS["gspn_ssm_forward"][1]) == g.GSPN_ERR_UNSUPPORTED
+    assert call("gspn_conv_forward", conv(B=4, L=1 << 29), CALLS["gspn_conv_forward"][1]) == g.GSPN_ERR_UNSUPPORTED
+    a = list(CALLS["gspn_conv_step"][1])
+    a[4] = 1 << 20
+    assert call("gspn_conv_step", conv(B=65536, L=1), a) == g.GSPN_ERR_UNSUPPORTED
+    assert call("gspn_norm_forward", norm(C=16385), CALLS["gspn_norm_forward"][1]) == g.GSPN_ERR_UNSUPPORTED
+    # five column sums of a wide row
+    assert call("gspn_norm_backward", norm(C=16384), CALLS["gspn_norm_backward"][1]) == g.GSPN_ERR_UNSUPPORTED
+
+
+def test_slots():
+    for name in ("gspn_conv_step", "gspn_ssm_step"):
+        make, args, _ = CALLS[name]
+        i = args.index(4)
+        a = list(args)
+        a[i] = 0
+        assert call(name, make(), a) == g.GSPN_ERR_INVALID_ARG
+        a[i], a[i - 1] = 1, None                                    # two rows, one slot, no index
+        assert call(name, make(), a) == g.GSPN_ERR_INVALID_ARG
+        assert call(name, make(L=2), args) == g.GSPN_ERR_INVALID_ARG
+
+
+def test_binding_refuses_host_tensors():
+    x, w = torch.zeros(1, 4, 8), torch.zeros(8, 4)
+    for f in (lambda: g.conv_forward(x, w), lambda: g.norm_forward(x), lambda: g.conv_step(x[0], w, None, torch.zeros(4, 3, 8)),
+              lambda: g.ssm_forward(x, x, torch.zeros(8, 2), torch.zeros(1, 4, 1, 2), torch.zeros(1, 4, 1, 2))):
+        with pytest.raises(ValueError):
+            f()
+    with pytest.raises(TypeError):
+        g.conv_forward(None, w)
+
+
+@pytest.mark.gpu
+def test_binding_refuses_wrong_tensors():
+    z = lambda *s, **k: torch.zeros(*s, device="cuda", **k)  # noqa: E731
+    x, w = z(2, 4, 8), z(8, 4)
+    A, B = z(8, 2), z(2, 4, 1, 2)
+    i32 = dict(dtype=torch.int32)
+    bad = [
+        (ValueError, lambda: g.conv_forward(x[0], w)), (ValueError, lambda: g.conv_forward(x, z(4, 8))),
+        (TypeError, lambda: g.conv_forward(x, w.bfloat16())), (TypeError, lambda: g.conv_forward(x.half(), w)),
+        (ValueError, lambda: g.conv_forward(x.transpose(1, 2), z(4, 4))), (ValueError, lambda: g.conv_forward(x, w, cu=z(3, **i32))),
+        (TypeError, lambda: g.conv_forward(x[:1], w, cu=z(3))), (ValueError, lambda: g.conv_forward(x, w, state0=z(2, 4, 8))),
+        (g.GspnError, lambda: g.conv_forward(x, z(8, 5))), (ValueError, lambda: g.conv_step(x[0], w, None, z(3, 3, 8))),
+        (TypeError, lambda: g.conv_step(x[0], w, None, z(4, 3, 8), idx=z(4).long())), (ValueError, lambda: g.conv_backward(x, w, None, x[:1])),
+        (ValueError, lambda: g.ssm_forward(x, x, A, B, z(2, 4, 1, 3))), (ValueError, lambda: g.ssm_forward(x, x, A, z(2, 4, 3, 2), B)),
+        (ValueError, lambda: g.ssm_forward(x, x, A, B, B, h0=z(1, 8, 2))), (TypeError, lambda: g.ssm_forward(x, x, A, B, B, D=z(8).bfloat16())),
+        (ValueError, lambda: g.ssm_forward(x, x[:, :3], A, B, B)), (g.GspnError, lambda: g.ssm_forward(x, x, z(8, 65), z(2, 4, 1, 65), z(2, 4, 1, 65))),
+        (ValueError, lambda: g.ssm_backward(x, x, A, B, B, x, z(3))), (ValueError, lambda: g.ssm_step(x[0], x[0], A, B[0], B[0], z(3, 8, 2))),
+        (ValueError, lambda: g.norm_forward(x, x, b_pre=z(8))), (TypeError, lambda: g.norm_forward(x.bfloat16(), x.half())),
+        (ValueError, lambda: g.norm_forward(x, x[:1])), (ValueError, lambda: g.norm_backward(x, x, None, x)),
+        (ValueError, lambda: g.norm_forward(x.transpose(0, 1).transpose(1, 2))),
+    ]
+    for k, (kind, f) in enumerate(bad):
+        with pytest.raises(kind):
+            f()
+            pytest.fail(f"call {k} was taken")
