@@ -51,23 +51,22 @@ struct SsmArgs {
 };
 
 // softplus(v) = max(v, 0) + log(1 + e), e = exp(-|v|), to a few 2^-24 relative: the exponential's
-// argument keeps its rounding error, and log(1 + e) = 2 atanh(s) with s = e / (2 + e) <= 1/3 by the
-// series in s^2 (seven terms leave 2e-8). A logarithm of 1 + e would lose the small steps.
-__device__ __forceinline__ float softplus_of(float v, float& e) {
+// argument keeps its rounding error, and log(1 + e) = 2 atanh(s) with s = e / (2 + e) <= 1/3, where
+// atanh(s) / s is a polynomial of degree 4 in s^2 (least largest error on [0, 1/9]: 4e-9). A logarithm
+// of 1 + e would lose the small steps.
+__device__ __forceinline__ float softplus_of(float v) {
     const float w = -fminf(fabsf(v), 88.f);
     const float t = w * kLog2e;
-    const float lo = fmaf(w, kLog2e, -t) + w * 1.925963033500e-8f;   // log2(e) - fp32(log2(e))
-    e = ex2(t);
+    const float lo = fmaf(w, kLog2e, -t);
+    float e = ex2(t);
     e = fmaf(e, lo * kLn2, e);
-    const float s = __fdividef(e, 2.f + e);
+    const float s = e * rcp(2.f + e);
     const float q = s * s;
-    float r = fmaf(q, 1.f / 13.f, 1.f / 11.f);
-    r = fmaf(r, q, 1.f / 9.f);
-    r = fmaf(r, q, 1.f / 7.f);
-    r = fmaf(r, q, 1.f / 5.f);
-    r = fmaf(r, q, 1.f / 3.f);
+    float r = fmaf(q, 0.14089168f, 0.13980301f);
+    r = fmaf(r, q, 0.20012455f);
+    r = fmaf(r, q, 0.33333157f);
     r = fmaf(r, q, 1.f);
-    const float out = fmaf(2.f * s, r, fmaxf(v, 0.f));
+    const float out = fmaf(s + s, r, fmaxf(v, 0.f));
     return v != v ? v : out;
 }
 
@@ -125,17 +124,37 @@ __device__ __forceinline__ void ld_part(uint4 (&r)[Part<T, NL>::NV], const void*
     }
 }
 
-// Four elements of the tile's B (or C): element e is token e / (4 NL), state e % (4 NL).
-template <typename T, int NL>
-__device__ __forceinline__ void ld_states(float (&r)[4], const void* base, long long row, long long tok,
-                                          const Place& q, int t0, int N) {
+// The same for the kFeed threads that feed a forward block.
+constexpr int kFeed = 128;
+template <typename T> struct Feed {
+    static constexpr int V = Vec<T>::V, VR = kCh / V, NV = kTile * VR / kFeed;
+};
+template <typename T>
+__device__ __forceinline__ void ld_feed(uint4 (&r)[Feed<T>::NV], const void* base, long long row, long long tok,
+                                        const Place& q, int t0, int tid, bool wide) {
+    using P = Feed<T>;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int e = i * 32 * NL + threadIdx.x;
+    for (int i = 0; i < P::NV; ++i) {
+        const int v = i * kFeed + tid;
+        const int t = t0 + v / P::VR, c = v % P::VR * P::V;
+        r[i] = make_uint4(0, 0, 0, 0);
+        if (t < q.hi) r[i] = ld_raw<T>((const T*)base + q.sp.row * row + (q.sp.first + t) * tok + q.c0 + c, q.nc - c, wide);
+    }
+}
+
+// A thread's elements of the tile's B (or C), as stored: conversions would wait for the loads here.
+// Element e of the tile is token e / (4 NL), state e % (4 NL); `n` threads share it.
+template <typename T, int NL, int E>
+__device__ __forceinline__ void ld_states(T (&r)[E], const void* base, long long row, long long tok, const Place& q,
+                                          int t0, int tid, int N) {
+    constexpr int threads = kTile * 4 * NL / E;
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+        const int e = i * threads + tid;
         const int t = t0 + e / (4 * NL), n = e % (4 * NL);
-        r[i] = t < q.hi && n < N
-                   ? Io<T>::ld((const T*)base + q.sp.row * row + (q.sp.first + t) * tok + (long long)q.g * N + n)
-                   : 0.f;
+        r[i] = T(0.f);
+        if (t < q.hi && n < N)
+            r[i] = ((const T*)base)[q.sp.row * row + (q.sp.first + t) * tok + (long long)q.g * N + n];
     }
 }
 
@@ -168,18 +187,181 @@ __device__ __forceinline__ void put_tokens(float* row0, int c, int nl, const flo
 }
 
 // ------------------------------------------------------------------------------------- forward
+// The block's first NL warps scan; four more feed them: they load the tokens, form d and d x, and turn
+// the sums over n of the tile before into y. The two work on neighbouring tiles, with one barrier a
+// tile, so the long latencies of the one side hide behind the other's arithmetic.
+// A token's shares of the sums over n, NL for each channel, with four floats between the vectors of
+// channels that one feeding thread adds up: its neighbours then start on other banks.
+template <typename T, int NL> struct YRow {
+    static constexpr int vec = Vec<T>::V * NL + 4, len = kCh / Vec<T>::V * vec;
+    static __device__ __forceinline__ int at(int c, int nl) { return c / Vec<T>::V * vec + c % Vec<T>::V * NL + nl; }
+    // the sum of channel c's shares; row is 16-byte aligned
+    static __device__ __forceinline__ float sum(const float* row, int c) {
+        const float* s = row + at(c, 0);
+        if constexpr (NL == 2) {
+            const float2 v = *(const float2*)s;
+            return v.x + v.y;
+        } else {
+            float w = 0.f;
+#pragma unroll
+            for (int k = 0; k < NL; k += 4) {
+                const float4 v = *(const float4*)(s + k);
+                w += (v.x + v.y) + (v.z + v.w);
+            }
+            return w;
+        }
+    }
+};
+
+// Shared memory moves 128 bytes a cycle, and 16-byte loads of a whole warp take four cycles even where
+// lanes read the same words, so what the scan loads for each token is kept small: d and d x as one
+// pair, B and C of bf16 inputs as stored. Rows of d have 16 bytes between the vectors of channels
+// that one feeding thread writes, which spreads its neighbours over the banks.
+template <typename T> struct DRow {
+    static constexpr int vec = Vec<T>::V + 2, len = kCh / Vec<T>::V * vec;     // in pairs
+    static __device__ __forceinline__ int at(int c) { return c / Vec<T>::V * vec + c % Vec<T>::V; }
+};
+// B[4], C[4] of a lane side by side.
+template <typename T> struct BC4 {
+    T v[8];
+};
+__device__ __forceinline__ void get_b(const BC4<float>& s, float (&b)[4]) {
+    const float4 q = *(const float4*)s.v;
+    b[0] = q.x; b[1] = q.y; b[2] = q.z; b[3] = q.w;
+}
+__device__ __forceinline__ void get_bc(const BC4<float>& s, float (&b)[4], float (&c)[4]) {
+    get_b(s, b);
+    const float4 q = *(const float4*)(s.v + 4);
+    c[0] = q.x; c[1] = q.y; c[2] = q.z; c[3] = q.w;
+}
+__device__ __forceinline__ void get_b(const BC4<__nv_bfloat16>& s, float (&b)[4]) {
+    const uint2 q = *(const uint2*)s.v;
+    b[0] = __uint_as_float(q.x << 16); b[1] = __uint_as_float(q.x & 0xffff0000u);
+    b[2] = __uint_as_float(q.y << 16); b[3] = __uint_as_float(q.y & 0xffff0000u);
+}
+__device__ __forceinline__ void get_bc(const BC4<__nv_bfloat16>& s, float (&b)[4], float (&c)[4]) {
+    float v[8];
+    unpack_raw<__nv_bfloat16>(*(const uint4*)s.v, v);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) { b[j] = v[j]; c[j] = v[4 + j]; }
+}
+
+template <typename T, int NL, bool LOCAL> struct FwdSmem {
+    float2 dd[2][kTile][DRow<T>::len];                 // d, d x
+    BC4<T> bc[2][kTile][NL];
+    float y[LOCAL ? 1 : 2][LOCAL ? 1 : kTile][YRow<T, NL>::len];   // each lane's share of the sums over n
+};
+
 // LOCAL: the first pass over pieces (from a zero state, the last piece left out).
 template <typename T, int NL, bool LOCAL>
-__global__ void __launch_bounds__(32 * NL) k_ssm_fwd(const SsmArgs p) {
-    using P = Part<T, NL>;
-    constexpr int V = P::V;
-    __shared__ __align__(16) float2 sdd[kTile][kCh];
-    __shared__ __align__(16) float sB[kTile][4 * NL];
-    __shared__ __align__(16) float sC[LOCAL ? 1 : kTile][4 * NL];
-    __shared__ __align__(16) float sY[LOCAL ? 1 : kTile][kYS];
+__global__ void __launch_bounds__(32 * NL + kFeed) k_ssm_fwd(const SsmArgs p) {
+    extern __shared__ __align__(16) unsigned char smem_raw[];
+    FwdSmem<T, NL, LOCAL>& sm = *(FwdSmem<T, NL, LOCAL>*)smem_raw;
 
     const Place q = place_of(p, LOCAL ? p.K - 1 : p.K, 0);
     if (!LOCAL && q.k > 0 && q.lo >= q.hi) return;
+    const int tiles = (q.hi - q.lo + kTile - 1) / kTile;
+
+    if (threadIdx.x >= 32 * NL) {
+        // ------------------------------------------------------------ feed
+        using P = Feed<T>;
+        constexpr int V = P::V, NS = NL;                          // elements of B (and of C) for each thread
+        const int tid = threadIdx.x - 32 * NL;
+        const int vc = tid % P::VR * V;
+        float bias[V], Dv[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            bias[i] = (p.bias && vc + i < q.nc) ? p.bias[q.c0 + vc + i] : 0.f;
+            Dv[i] = (!LOCAL && p.D && vc + i < q.nc) ? p.D[q.c0 + vc + i] : 0.f;
+        }
+        // x and z of the tile to be loaded, the one staged and the one before it
+        uint4 rx[P::NV], rd[P::NV], rz[P::NV], x1[P::NV], z1[P::NV], x0[P::NV], z0[P::NV];
+        T rB[NS], rC[NS];
+        auto load = [&](int i) {
+            const int t0 = q.lo + i * kTile;
+            ld_feed<T>(rx, p.x, p.x_row, p.x_tok, q, t0, tid, p.wide);
+            ld_feed<T>(rd, p.dt, p.dt_row, p.dt_tok, q, t0, tid, p.wide);
+            ld_states<T, NL>(rB, p.Bm, p.b_row, p.b_tok, q, t0, tid, p.N);
+            if constexpr (!LOCAL) {
+                if (p.z) ld_feed<T>(rz, p.z, p.z_row, p.z_tok, q, t0, tid, p.wide);
+                ld_states<T, NL>(rC, p.Cm, p.c_row, p.c_tok, q, t0, tid, p.N);
+            }
+        };
+        auto stage = [&](int i) {
+            const int t0 = q.lo + i * kTile, buf = i & 1;
+#pragma unroll
+            for (int k = 0; k < P::NV; ++k) {
+                const int t = (k * kFeed + tid) / P::VR;
+                x0[k] = x1[k];
+                z0[k] = z1[k];
+                x1[k] = rx[k];
+                z1[k] = rz[k];
+                float xv[V], dv[V];
+                float2 dd[V];
+                unpack_raw<T>(rx[k], xv);
+                unpack_raw<T>(rd[k], dv);
+                const bool ok = t0 + t < q.hi;
+#pragma unroll
+                for (int j = 0; j < V; ++j) {
+                    float d = dv[j] + bias[j];
+                    if (p.softplus) d = softplus_of(d);
+                    // a token behind the end makes no step, and the state stays; its x was read as zero, and so
+                    // were those of channels behind the last, whose states are zero
+                    dd[j] = make_float2(ok ? d : 0.f, ok ? d * xv[j] : 0.f);
+                }
+                float4* to = (float4*)&sm.dd[buf][t][DRow<T>::at(vc)];
+#pragma unroll
+                for (int j = 0; j < V; j += 2) to[j / 2] = make_float4(dd[j].x, dd[j].y, dd[j + 1].x, dd[j + 1].y);
+            }
+#pragma unroll
+            for (int k = 0; k < NS; ++k) {
+                const int e = k * kFeed + tid;
+                T* to = (&sm.bc[buf][0][0])[e / 4].v + e % 4;
+                to[0] = rB[k];
+                if constexpr (!LOCAL) to[4] = rC[k];
+            }
+        };
+        auto finish = [&](int i) {                                // i is the tile before the one staged last
+            const int t0 = q.lo + i * kTile, buf = i & 1;
+#pragma unroll
+            for (int k = 0; k < P::NV; ++k) {
+                const int t = (k * kFeed + tid) / P::VR;
+                if (t0 + t < q.hi) {
+                    float xv[V], zv[V], out[V];
+                    unpack_raw<T>(x0[k], xv);
+                    unpack_raw<T>(z0[k], zv);
+#pragma unroll
+                    for (int j = 0; j < V; ++j) {
+                        out[j] = fmaf(Dv[j], xv[j], YRow<T, NL>::sum(sm.y[buf][t], vc + j));
+                        if (p.z) out[j] *= silu(zv[j]);
+                    }
+                    st_vec<T>((T*)p.y + ((long long)q.sp.row * p.L + q.sp.first + t0 + t) * p.C + q.c0 + vc, out,
+                              q.nc - vc, p.wide);
+                }
+            }
+        };
+        if (tiles > 0) {
+            load(0);
+            stage(0);
+            if (tiles > 1) load(1);
+        }
+        __syncthreads();
+        for (int i = 0; i < tiles; ++i) {
+            if (i + 1 < tiles) {
+                stage(i + 1);
+                if (i + 2 < tiles) load(i + 2);
+            } else {
+#pragma unroll
+                for (int k = 0; k < P::NV; ++k) { x0[k] = x1[k]; z0[k] = z1[k]; }
+            }
+            __syncthreads();
+            // the sums of tile i are complete; its buffer is written again behind the next barrier only
+            if constexpr (!LOCAL) finish(i);
+        }
+        return;
+    }
+
+    // ---------------------------------------------------------------- scan
     const int lane = threadIdx.x & 31, nl = lane % NL;
     const int cl = (threadIdx.x >> 5) * (32 / NL) + lane / NL;    // channel within the block
     const bool cok = cl < q.nc;
@@ -215,122 +397,60 @@ __global__ void __launch_bounds__(32 * NL) k_ssm_fwd(const SsmArgs p) {
             }
         }
     }
-
-    // The thread's own vector of channels in the staging and in the epilogue.
-    const int vc = threadIdx.x % P::VR * V;
-    float bias[V], Dv[V];
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-        bias[i] = (p.bias && vc + i < q.nc) ? p.bias[q.c0 + vc + i] : 0.f;
-        Dv[i] = (!LOCAL && p.D && vc + i < q.nc) ? p.D[q.c0 + vc + i] : 0.f;
-    }
+    f2 h01 = pack(h[0], h[1]), h23 = pack(h[2], h[3]);
     const long long save0 = LOCAL ? 0 : save_slot(p, q.sp, q.s);
-
-    uint4 rx[P::NV], rd[P::NV], rz[P::NV], kx[P::NV], kz[P::NV];
-    float rB[4], rC[4];
-    auto load = [&](int t0) {
-        ld_part<T, NL>(rx, p.x, p.x_row, p.x_tok, q, t0, p.wide);
-        ld_part<T, NL>(rd, p.dt, p.dt_row, p.dt_tok, q, t0, p.wide);
-        ld_states<T, NL>(rB, p.Bm, p.b_row, p.b_tok, q, t0, p.N);
-        if constexpr (!LOCAL) {
-            if (p.z) ld_part<T, NL>(rz, p.z, p.z_row, p.z_tok, q, t0, p.wide);
-            ld_states<T, NL>(rC, p.Cm, p.c_row, p.c_tok, q, t0, p.N);
-        }
-    };
     float sum_d = 0.f;
-    if (q.lo < q.hi) load(q.lo);
-    for (int t0 = q.lo; t0 < q.hi; t0 += kTile) {
-#pragma unroll
-        for (int i = 0; i < P::NV; ++i) {
-            const int v = i * P::threads + threadIdx.x;
-            kx[i] = rx[i];
-            kz[i] = rz[i];
-            if (v < P::vecs) {
-                const int t = v / P::VR;
-                float xv[V], dv[V];
-                unpack_raw<T>(rx[i], xv);
-                unpack_raw<T>(rd[i], dv);
-                const bool ok = t0 + t < q.hi;
-#pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    float e, d = dv[j] + bias[j];
-                    if (p.softplus) d = softplus_of(d, e);
-                    // a token behind the end or a channel behind the last: no step, the state stays
-                    d = ok && vc + j < q.nc ? d : 0.f;
-                    sdd[t][vc + j] = make_float2(d, ok ? d * xv[j] : 0.f);
-                }
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int e = i * P::threads + threadIdx.x;
-            (&sB[0][0])[e] = rB[i];
-            if constexpr (!LOCAL) (&sC[0][0])[e] = rC[i];
-        }
-        __syncthreads();
-        if (t0 + kTile < q.hi) load(t0 + kTile);
-#pragma unroll
-        for (int t = 0; t < kTile; t += 4) {
-            if constexpr (!LOCAL) {
-                if (t % kSub == 0 && p.hsave && keeps && t0 + t < q.hi)
-                    *(float4*)(p.hsave + ((save0 + (t0 + t) / kSub) * p.C + c) * p.Np + n0) =
-                        make_float4(h[0], h[1], h[2], h[3]);
-            }
-            float yv[4];
+    __syncthreads();
+    for (int i = 0; i < tiles; ++i) {
+        const int t0 = q.lo + i * kTile, buf = i & 1;
+        // Operands of four tokens are fetched while the four before are worked on; the stores below would
+        // otherwise hold back the loads behind them.
+        float2 dd[2][4];
+        BC4<T> bc[2][4];
+        auto fetch = [&](int t, int w) {
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
-                const float2 dd = sdd[t + u][cl];
-                const float4 b = *(const float4*)&sB[t + u][n0];
-                const float bb[4] = {b.x, b.y, b.z, b.w};
-                if constexpr (LOCAL) {
-                    sum_d += dd.x;
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) h[j] = fmaf(ex2(dd.x * A2[j]), h[j], dd.y * bb[j]);
-                } else {
-                    const float4 cc4 = *(const float4*)&sC[t + u][n0];
-                    const float cc[4] = {cc4.x, cc4.y, cc4.z, cc4.w};
-                    yv[u] = 0.f;
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        h[j] = fmaf(ex2(dd.x * A2[j]), h[j], dd.y * bb[j]);
-                        yv[u] = fmaf(h[j], cc[j], yv[u]);
-                    }
-                }
+                dd[w][u] = sm.dd[buf][t + u][DRow<T>::at(cl)];
+                bc[w][u] = sm.bc[buf][t + u][nl];
             }
+        };
+        fetch(0, 0);
+#pragma unroll
+        for (int t = 0; t < kTile; t += 4) {
+            const int w = t / 4 & 1;
+            if (t + 4 < kTile) fetch(t + 4, w ^ 1);
             if constexpr (!LOCAL) {
-                float r[2];
-                reduce_tokens<NL>(yv, nl, r);
-                put_tokens<NL>(&sY[t][0], cl, nl, r);
+                if (t % kSub == 0 && p.hsave && keeps && t0 + t < q.hi)
+                    *(ulonglong2*)(p.hsave + ((save0 + (t0 + t) / kSub) * p.C + c) * p.Np + n0) = make_ulonglong2(h01, h23);
+            }
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const float d = dd[w][u].x, dx = dd[w][u].y;
+                float b[4], cc[4];
+                if constexpr (LOCAL) get_b(bc[w][u], b);
+                else get_bc(bc[w][u], b, cc);
+                const f2 a01 = pack(ex2(d * A2[0]), ex2(d * A2[1])), a23 = pack(ex2(d * A2[2]), ex2(d * A2[3]));
+                h01 = fma2(a01, h01, pack(dx * b[0], dx * b[1]));
+                h23 = fma2(a23, h23, pack(dx * b[2], dx * b[3]));
+                if constexpr (LOCAL) {
+                    sum_d += d;
+                } else {
+                    const float2 s = unpack(fma2(h01, pack(cc[0], cc[1]), mul2(h23, pack(cc[2], cc[3]))));
+                    sm.y[buf][t + u][YRow<T, NL>::at(cl, nl)] = s.x + s.y;
+                }
             }
         }
         __syncthreads();
-        if constexpr (!LOCAL) {
-#pragma unroll
-            for (int i = 0; i < P::NV; ++i) {
-                const int v = i * P::threads + threadIdx.x;
-                const int t = v / P::VR;
-                if (v < P::vecs && t0 + t < q.hi) {
-                    float xv[V], zv[V], out[V];
-                    unpack_raw<T>(kx[i], xv);
-                    unpack_raw<T>(kz[i], zv);
-#pragma unroll
-                    for (int j = 0; j < V; ++j) {
-                        out[j] = fmaf(Dv[j], xv[j], sY[t][vc + j]);
-                        if (p.z) out[j] *= silu(zv[j]);
-                    }
-                    st_vec<T>((T*)p.y + ((long long)q.sp.row * p.L + q.sp.first + t0 + t) * p.C + q.c0 + vc, out,
-                              q.nc - vc, p.wide);
-                }
-            }
-        }
     }
     if constexpr (LOCAL) {
-        if (keeps) *(float4*)(p.loc + ((piece0 + q.k + 1) * p.C + c) * p.Np + n0) = make_float4(h[0], h[1], h[2], h[3]);
+        if (keeps) *(ulonglong2*)(p.loc + ((piece0 + q.k + 1) * p.C + c) * p.Np + n0) = make_ulonglong2(h01, h23);
         if (cok && nl == 0) p.sdt[((long long)q.s * p.K + q.k) * p.C + c] = sum_d;
     } else if (p.h && q.k == q.last) {
+        const float2 u = unpack(h01), v = unpack(h23);
+        const float f[4] = {u.x, u.y, v.x, v.y};
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-            if (cok && n0 + j < p.N) p.h[((long long)q.s * p.C + c) * p.N + n0 + j] = h[j];
+            if (cok && n0 + j < p.N) p.h[((long long)q.s * p.C + c) * p.N + n0 + j] = f[j];
     }
 }
 
@@ -392,12 +512,12 @@ __global__ void __launch_bounds__(32 * NL) k_ssm_bwd_local(const SsmArgs p) {
 #pragma unroll
     for (int i = 0; i < V; ++i) bias[i] = (p.bias && vc + i < q.nc) ? p.bias[q.c0 + vc + i] : 0.f;
     uint4 rd[P::NV], rz[P::NV], rg[P::NV];
-    float rC[4];
+    T rC[4];
     auto load = [&](int t0) {
         ld_part<T, NL>(rd, p.dt, p.dt_row, p.dt_tok, q, t0, p.wide);
         ld_part<T, NL>(rg, p.dy, (long long)p.L * p.C, p.C, q, t0, p.wide);
         if (p.z) ld_part<T, NL>(rz, p.z, p.z_row, p.z_tok, q, t0, p.wide);
-        ld_states<T, NL>(rC, p.Cm, p.c_row, p.c_tok, q, t0, p.N);
+        ld_states<T, NL>(rC, p.Cm, p.c_row, p.c_tok, q, t0, threadIdx.x, p.N);
     };
     float sum_d = 0.f;
     int t0 = q.lo + (q.hi - q.lo + kTile - 1) / kTile * kTile - kTile;
@@ -415,8 +535,8 @@ __global__ void __launch_bounds__(32 * NL) k_ssm_bwd_local(const SsmArgs p) {
                 const bool ok = t0 + t < q.hi;
 #pragma unroll
                 for (int j = 0; j < V; ++j) {
-                    float e, d = dv[j] + bias[j];
-                    if (p.softplus) d = softplus_of(d, e);
+                    float d = dv[j] + bias[j];
+                    if (p.softplus) d = softplus_of(d);
                     d = ok && vc + j < q.nc ? d : 0.f;
                     const float r = p.z ? gv[j] * silu(zv[j]) : gv[j];
                     sdr[t][vc + j] = make_float2(d, ok ? r : 0.f);
@@ -424,7 +544,7 @@ __global__ void __launch_bounds__(32 * NL) k_ssm_bwd_local(const SsmArgs p) {
             }
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) (&sC[0][0])[i * P::threads + threadIdx.x] = rC[i];
+        for (int i = 0; i < 4; ++i) (&sC[0][0])[i * P::threads + threadIdx.x] = Io<T>::ld(&rC[i]);
         __syncthreads();
         if (t0 - kTile >= q.lo) load(t0 - kTile);
 #pragma unroll 8
@@ -491,15 +611,15 @@ __global__ void __launch_bounds__(32 * NL) k_ssm_bwd(const SsmArgs p) {
     const int cbk = q.cb % p.nb;
 
     uint4 rx[P::NV], rd[P::NV], rz[P::NV], rg[P::NV];
-    float rB[4], rC[4];
+    T rB[4], rC[4];
     float4 rh[2];
     auto load = [&](int t0) {
         ld_part<T, NL>(rx, p.x, p.x_row, p.x_tok, q, t0, p.wide);
         ld_part<T, NL>(rd, p.dt, p.dt_row, p.dt_tok, q, t0, p.wide);
         ld_part<T, NL>(rg, p.dy, (long long)p.L * p.C, p.C, q, t0, p.wide);
         if (p.z) ld_part<T, NL>(rz, p.z, p.z_row, p.z_tok, q, t0, p.wide);
-        ld_states<T, NL>(rB, p.Bm, p.b_row, p.b_tok, q, t0, p.N);
-        ld_states<T, NL>(rC, p.Cm, p.c_row, p.c_tok, q, t0, p.N);
+        ld_states<T, NL>(rB, p.Bm, p.b_row, p.b_tok, q, t0, threadIdx.x, p.N);
+        ld_states<T, NL>(rC, p.Cm, p.c_row, p.c_tok, q, t0, threadIdx.x, p.N);
 #pragma unroll
         for (int s = 0; s < 2; ++s)
             rh[s] = keeps && t0 + s * kSub < q.hi
@@ -528,8 +648,8 @@ __global__ void __launch_bounds__(32 * NL) k_ssm_bwd(const SsmArgs p) {
                 const bool ok = t0 + t < q.hi;
 #pragma unroll
                 for (int j = 0; j < V; ++j) {
-                    float e, d = dv[j] + bias_of(j);
-                    if (p.softplus) d = softplus_of(d, e);
+                    float d = dv[j] + bias_of(j);
+                    if (p.softplus) d = softplus_of(d);
                     d = ok && vc + j < q.nc ? d : 0.f;
                     sm.dd[t][vc + j] = make_float2(d, ok ? d * xv[j] : 0.f);
                     const float r = p.z ? gv[j] * silu(zv[j]) : gv[j];
@@ -543,8 +663,8 @@ __global__ void __launch_bounds__(32 * NL) k_ssm_bwd(const SsmArgs p) {
             const int t = e / (4 * NL), n = e % (4 * NL);
 #pragma unroll
             for (int m = 0; m < PC; ++m) {
-                sm.B[t][m][n ^ m] = rB[i];
-                sm.C[t][m][n ^ m] = rC[i];
+                sm.B[t][m][n ^ m] = Io<T>::ld(&rB[i]);
+                sm.C[t][m][n ^ m] = Io<T>::ld(&rC[i]);
             }
         }
         const float4 hin[2] = {rh[0], rh[1]};
@@ -784,8 +904,7 @@ __global__ void k_ssm_step(const SsmArgs p, const int* idx, int slots, int NL) {
             d = Io<T>::ld((const T*)p.dt + b * p.dt_row + c) + (p.bias ? p.bias[c] : 0.f);
             if (p.z) z = Io<T>::ld((const T*)p.z + b * p.z_row + c);
         }
-        float e;
-        if (p.softplus) d = softplus_of(d, e);
+        if (p.softplus) d = softplus_of(d);
         float y = 0.f;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -945,13 +1064,19 @@ gspn_status gspn_ssm_forward(const gspn_ssm_desc* desc, const void* x, const voi
     p.wide = (p.C / p.G * es) % 16 == 0 && wide_ok(x, p.x_row, p.x_tok, es) && wide_ok(dt, p.dt_row, p.dt_tok, es) &&
              (!z || wide_ok(z, p.z_row, p.z_tok, es)) && aligned_to(y, 16);
     cudaStream_t st = (cudaStream_t)stream;
+    cudaError_t e = cudaSuccess;
     with_lanes(desc->dtype, lanes_for(p.N), [&](auto t, auto nl) {
         using T = decltype(t);
         constexpr int NL = decltype(nl)::value;
         const unsigned cblocks = p.nb * p.G;
-        if (p.K > 1) k_ssm_fwd<T, NL, true><<<cblocks * (p.K - 1) * p.S, 32 * NL, 0, st>>>(p);
-        k_ssm_fwd<T, NL, false><<<cblocks * p.K * p.S, 32 * NL, 0, st>>>(p);
+        auto go = [&](auto kernel, size_t smem, unsigned pieces) {
+            if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+            if (e == cudaSuccess) kernel<<<cblocks * pieces * p.S, 32 * NL + kFeed, smem, st>>>(p);
+        };
+        if (p.K > 1) go(k_ssm_fwd<T, NL, true>, sizeof(FwdSmem<T, NL, true>), p.K - 1);
+        go(k_ssm_fwd<T, NL, false>, sizeof(FwdSmem<T, NL, false>), p.K);
     });
+    if (e != cudaSuccess) return GSPN_ERR_CUDA;
     return last_status();
 }
 
