@@ -26,14 +26,13 @@ namespace {
 constexpr int kCh = 32;      // channels of a block
 constexpr int kTile = 32;    // tokens staged at once
 constexpr int kSub = 16;     // tokens between saved states
-constexpr int kYS = 40;      // row stride of the per-token sums: four rows of eight channels miss each other's banks
 constexpr int kMaxN = 64;
 
 struct SsmArgs {
     int B, L, C, G, N, S;    // S: sequences (packed or rows)
     int Np;                  // N rounded up to 4
     int K;                   // pieces of a sequence
-    int nb;                  // channel blocks of a group
+    int nb, nbb;             // channel blocks of a group; of a backward block's size
     int softplus;
     bool wide;               // x, dt, z, y (and dy and the gradients) have 16-byte aligned vectors
     const void *x, *dt, *z, *Bm, *Cm;
@@ -54,21 +53,23 @@ struct SsmArgs {
 // argument keeps its rounding error, and log(1 + e) = 2 atanh(s) with s = e / (2 + e) <= 1/3, where
 // atanh(s) / s is a polynomial of degree 4 in s^2 (least largest error on [0, 1/9]: 4e-9). A logarithm
 // of 1 + e would lose the small steps.
-__device__ __forceinline__ float softplus_of(float v) {
-    const float w = -fminf(fabsf(v), 88.f);
-    const float t = w * kLog2e;
-    const float lo = fmaf(w, kLog2e, -t);
-    float e = ex2(t);
-    e = fmaf(e, lo * kLn2, e);
-    const float s = e * rcp(2.f + e);
-    const float q = s * s;
-    float r = fmaf(q, 0.14089168f, 0.13980301f);
-    r = fmaf(r, q, 0.20012455f);
-    r = fmaf(r, q, 0.33333157f);
-    r = fmaf(r, q, 1.f);
-    const float out = fmaf(s + s, r, fmaxf(v, 0.f));
-    return v != v ? v : out;
+// Two at a time: issue slots are what the staging costs.
+__device__ __forceinline__ float2 softplus_of(float2 v) {
+    const f2 w = pack(-fminf(fabsf(v.x), 88.f), -fminf(fabsf(v.y), 88.f));
+    const f2 t = mul2(w, both(kLog2e));
+    const f2 lo = fma2(w, both(kLog2e), mul2(t, both(-1.f)));
+    f2 e = ex2_2(t);
+    e = fma2(e, mul2(lo, both(kLn2)), e);
+    const float2 den = unpack(add2(e, both(2.f)));
+    const f2 s = mul2(e, pack(rcp(den.x), rcp(den.y)));
+    const f2 q = mul2(s, s);
+    f2 r = fma2(q, both(0.14089168f), both(0.13980301f));
+    r = fma2(r, q, both(0.20012455f));
+    r = fma2(r, q, both(0.33333157f));
+    r = fma2(r, q, both(1.f));
+    return unpack(fma2(add2(s, s), r, pack(max_nan(v.x, 0.f), max_nan(v.y, 0.f))));
 }
+__device__ __forceinline__ float softplus_of(float v) { return softplus_of(make_float2(v, v)).x; }
 
 // Tokens of a piece: equal pieces, whole runs of kSub tokens so that saved states fall on borders.
 __device__ __forceinline__ int piece_len(int len, int K) {
@@ -85,17 +86,17 @@ struct Place {
     int s, k, cb, g, c0, nc, lo, hi, last;   // sequence, piece, channel block; tokens [lo, hi) of the sequence
     Span sp;
 };
-__device__ __forceinline__ Place place_of(const SsmArgs& p, int pieces, int first_piece) {
+__device__ __forceinline__ Place place_of(const SsmArgs& p, int pieces, int first_piece, int ch, int nb) {
     Place q;
-    const int cblocks = p.nb * p.G;
+    const int cblocks = nb * p.G;
     q.cb = blockIdx.x % cblocks;
     const int sk = blockIdx.x / cblocks;
     q.k = sk % pieces + first_piece;
     q.s = sk / pieces;
-    q.g = q.cb / p.nb;
+    q.g = q.cb / nb;
     const int Cg = p.C / p.G;
-    q.c0 = q.g * Cg + (q.cb % p.nb) * kCh;
-    q.nc = min(kCh, (q.g + 1) * Cg - q.c0);
+    q.c0 = q.g * Cg + (q.cb % nb) * ch;
+    q.nc = min(ch, (q.g + 1) * Cg - q.c0);
     q.sp = span_of(p.cu, q.s, p.L);
     const int cl = piece_len(q.sp.len, p.K);
     q.lo = (int)min((long long)q.k * cl, (long long)q.sp.len);
@@ -124,21 +125,21 @@ __device__ __forceinline__ void ld_part(uint4 (&r)[Part<T, NL>::NV], const void*
     }
 }
 
-// The same for the kFeed threads that feed a forward block.
-constexpr int kFeed = 128;
-template <typename T> struct Feed {
-    static constexpr int V = Vec<T>::V, VR = kCh / V, NV = kTile * VR / kFeed;
+// The same for the threads that feed a forward block: four channels each, NV times over. Eight warps:
+// with four, one on each scheduler, their latencies took longer than the scan of a tile.
+constexpr int kQ = 4, kVR = kCh / kQ;
+template <int NL> struct Feed {
+    static constexpr int threads = NL == 16 ? 128 : 256, NV = kTile * kVR / threads;
 };
-template <typename T>
-__device__ __forceinline__ void ld_feed(uint4 (&r)[Feed<T>::NV], const void* base, long long row, long long tok,
-                                        const Place& q, int t0, int tid, bool wide) {
-    using P = Feed<T>;
+template <typename T, int NL>
+__device__ __forceinline__ void ld_feed(typename Quad<T>::raw (&r)[Feed<NL>::NV], const void* base, long long row,
+                                        long long tok, const Place& q, int t0, int tid, bool wide) {
 #pragma unroll
-    for (int i = 0; i < P::NV; ++i) {
-        const int v = i * kFeed + tid;
-        const int t = t0 + v / P::VR, c = v % P::VR * P::V;
-        r[i] = make_uint4(0, 0, 0, 0);
-        if (t < q.hi) r[i] = ld_raw<T>((const T*)base + q.sp.row * row + (q.sp.first + t) * tok + q.c0 + c, q.nc - c, wide);
+    for (int i = 0; i < Feed<NL>::NV; ++i) {
+        const int v = i * Feed<NL>::threads + tid;
+        const int t = t0 + v / kVR, c = v % kVR * kQ;
+        r[i] = typename Quad<T>::raw{};
+        if (t < q.hi) r[i] = ld_quad((const T*)base + q.sp.row * row + (q.sp.first + t) * tok + q.c0 + c, q.nc - c, wide);
     }
 }
 
@@ -158,43 +159,15 @@ __device__ __forceinline__ void ld_states(T (&r)[E], const void* base, long long
     }
 }
 
-// Sums over the NL lanes of a channel for four tokens at once. NL >= 4: returns token (nl & 3)'s sum
-// in r[0]; NL = 2: tokens 2 (nl & 1) and the next in r[0], r[1].
-template <int NL>
-__device__ __forceinline__ void reduce_tokens(const float (&v)[4], int nl, float (&r)[2]) {
-    constexpr unsigned all = 0xffffffffu;
-    if constexpr (NL == 2) {
-        const bool up = nl & 1;
-        r[0] = (up ? v[2] : v[0]) + __shfl_xor_sync(all, up ? v[0] : v[2], 1);
-        r[1] = (up ? v[3] : v[1]) + __shfl_xor_sync(all, up ? v[1] : v[3], 1);
-    } else {
-        const bool hi = nl & 2, up = nl & 1;
-        const float a = (hi ? v[2] : v[0]) + __shfl_xor_sync(all, hi ? v[0] : v[2], 2);
-        const float b = (hi ? v[3] : v[1]) + __shfl_xor_sync(all, hi ? v[1] : v[3], 2);
-        r[0] = (up ? b : a) + __shfl_xor_sync(all, up ? a : b, 1);
-        if constexpr (NL >= 8) r[0] += __shfl_xor_sync(all, r[0], 4);
-        if constexpr (NL >= 16) r[0] += __shfl_xor_sync(all, r[0], 8);
-    }
-}
-template <int NL>
-__device__ __forceinline__ void put_tokens(float* row0, int c, int nl, const float (&r)[2]) {
-    if constexpr (NL == 2) {
-        row0[(2 * (nl & 1)) * kYS + c] = r[0];
-        row0[(2 * (nl & 1) + 1) * kYS + c] = r[1];
-    } else {
-        if (nl < 4) row0[nl * kYS + c] = r[0];
-    }
-}
-
 // ------------------------------------------------------------------------------------- forward
-// The block's first NL warps scan; four more feed them: they load the tokens, form d and d x, and turn
+// The block's first NL warps scan; eight more (four for NL = 16) feed them: they load the tokens, form d and d x, and turn
 // the sums over n of the tile before into y. The two work on neighbouring tiles, with one barrier a
 // tile, so the long latencies of the one side hide behind the other's arithmetic.
 // A token's shares of the sums over n, NL for each channel, with four floats between the vectors of
 // channels that one feeding thread adds up: its neighbours then start on other banks.
-template <typename T, int NL> struct YRow {
-    static constexpr int vec = Vec<T>::V * NL + 4, len = kCh / Vec<T>::V * vec;
-    static __device__ __forceinline__ int at(int c, int nl) { return c / Vec<T>::V * vec + c % Vec<T>::V * NL + nl; }
+template <int NL> struct YRow {
+    static constexpr int vec = kQ * NL + 4, len = kVR * vec;
+    static __device__ __forceinline__ int at(int c, int nl) { return c / kQ * vec + c % kQ * NL + nl; }
     // the sum of channel c's shares; row is 16-byte aligned
     static __device__ __forceinline__ float sum(const float* row, int c) {
         const float* s = row + at(c, 0);
@@ -205,8 +178,10 @@ template <typename T, int NL> struct YRow {
             float w = 0.f;
 #pragma unroll
             for (int k = 0; k < NL; k += 4) {
-                const float4 v = *(const float4*)(s + k);
-                w += (v.x + v.y) + (v.z + v.w);
+                f2 a, b;
+                ld_pairs(s + k, a, b);
+                const float2 v = unpack(add2(a, b));
+                w += v.x + v.y;
             }
             return w;
         }
@@ -214,12 +189,13 @@ template <typename T, int NL> struct YRow {
 };
 
 // Shared memory moves 128 bytes a cycle, and 16-byte loads of a whole warp take four cycles even where
-// lanes read the same words, so what the scan loads for each token is kept small: d and d x as one
-// pair, B and C of bf16 inputs as stored. Rows of d have 16 bytes between the vectors of channels
-// that one feeding thread writes, which spreads its neighbours over the banks.
-template <typename T> struct DRow {
-    static constexpr int vec = Vec<T>::V + 2, len = kCh / Vec<T>::V * vec;     // in pairs
-    static __device__ __forceinline__ int at(int c) { return c / Vec<T>::V * vec + c % Vec<T>::V; }
+// lanes read the same words: a token costs a warp four of them for d, d, d x, d x (doubled, so that the
+// two-wide products need no moves) and four for B and C of bf16 inputs, which stay as stored. Rows of
+// d have 16 bytes between the vectors of channels that one feeding thread writes, which spreads its
+// neighbours over the banks.
+struct DRow {
+    static constexpr int vec = kQ + 1, len = kVR * vec;     // in entries of 16 bytes
+    static __device__ __forceinline__ int at(int c) { return c / kQ * vec + c % kQ; }
 };
 // B[4], C[4] of a lane side by side.
 template <typename T> struct BC4 {
@@ -246,44 +222,50 @@ __device__ __forceinline__ void get_bc(const BC4<__nv_bfloat16>& s, float (&b)[4
     for (int j = 0; j < 4; ++j) { b[j] = v[j]; c[j] = v[4 + j]; }
 }
 
+// Two blocks of NL = 4 fit an SM at 80 registers a thread; the scan needs more, the feed less.
+constexpr int kScanRegs4 = 112, kFeedRegs4 = 64, kFwdThreads4 = 128 + Feed<4>::threads;
+constexpr int kFwdRegs4 = 128 * kScanRegs4 + Feed<4>::threads * kFeedRegs4;
+
 template <typename T, int NL, bool LOCAL> struct FwdSmem {
-    float2 dd[2][kTile][DRow<T>::len];                 // d, d x
+    float4 dd[2][kTile][DRow::len];                 // d, d, d x, d x
     BC4<T> bc[2][kTile][NL];
-    float y[LOCAL ? 1 : 2][LOCAL ? 1 : kTile][YRow<T, NL>::len];   // each lane's share of the sums over n
+    float y[LOCAL ? 1 : 2][LOCAL ? 1 : kTile][YRow<NL>::len];   // each lane's share of the sums over n
 };
 
 // LOCAL: the first pass over pieces (from a zero state, the last piece left out).
 template <typename T, int NL, bool LOCAL>
-__global__ void __launch_bounds__(32 * NL + kFeed) k_ssm_fwd(const SsmArgs p) {
+__global__ void __launch_bounds__(32 * NL + Feed<NL>::threads, NL == 4 ? 2 : 1) k_ssm_fwd(const SsmArgs p) {
     extern __shared__ __align__(16) unsigned char smem_raw[];
     FwdSmem<T, NL, LOCAL>& sm = *(FwdSmem<T, NL, LOCAL>*)smem_raw;
 
-    const Place q = place_of(p, LOCAL ? p.K - 1 : p.K, 0);
+    const Place q = place_of(p, LOCAL ? p.K - 1 : p.K, 0, kCh, p.nb);
     if (!LOCAL && q.k > 0 && q.lo >= q.hi) return;
     const int tiles = (q.hi - q.lo + kTile - 1) / kTile;
 
     if (threadIdx.x >= 32 * NL) {
         // ------------------------------------------------------------ feed
-        using P = Feed<T>;
-        constexpr int V = P::V, NS = NL;                          // elements of B (and of C) for each thread
+        if constexpr (NL == 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFeedRegs4));
+        using P = Feed<NL>;
+        typedef typename Quad<T>::raw Raw;
+        constexpr int NS = kTile * 4 * NL / P::threads;           // elements of B (and of C) for each thread
         const int tid = threadIdx.x - 32 * NL;
-        const int vc = tid % P::VR * V;
-        float bias[V], Dv[V];
+        const int vc = tid % kVR * kQ;
+        float bias[kQ], Dv[kQ];
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
+        for (int i = 0; i < kQ; ++i) {
             bias[i] = (p.bias && vc + i < q.nc) ? p.bias[q.c0 + vc + i] : 0.f;
             Dv[i] = (!LOCAL && p.D && vc + i < q.nc) ? p.D[q.c0 + vc + i] : 0.f;
         }
         // x and z of the tile to be loaded, the one staged and the one before it
-        uint4 rx[P::NV], rd[P::NV], rz[P::NV], x1[P::NV], z1[P::NV], x0[P::NV], z0[P::NV];
+        Raw rx[P::NV], rd[P::NV], rz[P::NV], x1[P::NV], z1[P::NV], x0[P::NV], z0[P::NV];
         T rB[NS], rC[NS];
         auto load = [&](int i) {
             const int t0 = q.lo + i * kTile;
-            ld_feed<T>(rx, p.x, p.x_row, p.x_tok, q, t0, tid, p.wide);
-            ld_feed<T>(rd, p.dt, p.dt_row, p.dt_tok, q, t0, tid, p.wide);
+            ld_feed<T, NL>(rx, p.x, p.x_row, p.x_tok, q, t0, tid, p.wide);
+            ld_feed<T, NL>(rd, p.dt, p.dt_row, p.dt_tok, q, t0, tid, p.wide);
             ld_states<T, NL>(rB, p.Bm, p.b_row, p.b_tok, q, t0, tid, p.N);
             if constexpr (!LOCAL) {
-                if (p.z) ld_feed<T>(rz, p.z, p.z_row, p.z_tok, q, t0, tid, p.wide);
+                if (p.z) ld_feed<T, NL>(rz, p.z, p.z_row, p.z_tok, q, t0, tid, p.wide);
                 ld_states<T, NL>(rC, p.Cm, p.c_row, p.c_tok, q, t0, tid, p.N);
             }
         };
@@ -291,31 +273,31 @@ __global__ void __launch_bounds__(32 * NL + kFeed) k_ssm_fwd(const SsmArgs p) {
             const int t0 = q.lo + i * kTile, buf = i & 1;
 #pragma unroll
             for (int k = 0; k < P::NV; ++k) {
-                const int t = (k * kFeed + tid) / P::VR;
+                const int t = (k * P::threads + tid) / kVR;
                 x0[k] = x1[k];
                 z0[k] = z1[k];
                 x1[k] = rx[k];
                 z1[k] = rz[k];
-                float xv[V], dv[V];
-                float2 dd[V];
-                unpack_raw<T>(rx[k], xv);
-                unpack_raw<T>(rd[k], dv);
+                float xv[kQ], dv[kQ];
+                unpack_quad(rx[k], xv);
+                unpack_quad(rd[k], dv);
+                // A token behind the end makes no step, and the state stays; its x was read as zero, and so were
+                // those of channels behind the last, whose states are zero.
                 const bool ok = t0 + t < q.hi;
+                float4* to = &sm.dd[buf][t][DRow::at(vc)];
 #pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    float d = dv[j] + bias[j];
+                for (int j = 0; j < kQ; j += 2) {
+                    float2 d = make_float2(dv[j] + bias[j], dv[j + 1] + bias[j + 1]);
                     if (p.softplus) d = softplus_of(d);
-                    // a token behind the end makes no step, and the state stays; its x was read as zero, and so
-                    // were those of channels behind the last, whose states are zero
-                    dd[j] = make_float2(ok ? d : 0.f, ok ? d * xv[j] : 0.f);
+                    if (!ok) d = make_float2(0.f, 0.f);
+                    const float2 w = unpack(mul2(pack(d.x, d.y), pack(xv[j], xv[j + 1])));
+                    to[j] = make_float4(d.x, d.x, w.x, w.x);
+                    to[j + 1] = make_float4(d.y, d.y, w.y, w.y);
                 }
-                float4* to = (float4*)&sm.dd[buf][t][DRow<T>::at(vc)];
-#pragma unroll
-                for (int j = 0; j < V; j += 2) to[j / 2] = make_float4(dd[j].x, dd[j].y, dd[j + 1].x, dd[j + 1].y);
             }
 #pragma unroll
             for (int k = 0; k < NS; ++k) {
-                const int e = k * kFeed + tid;
+                const int e = k * P::threads + tid;
                 T* to = (&sm.bc[buf][0][0])[e / 4].v + e % 4;
                 to[0] = rB[k];
                 if constexpr (!LOCAL) to[4] = rC[k];
@@ -325,17 +307,17 @@ __global__ void __launch_bounds__(32 * NL + kFeed) k_ssm_fwd(const SsmArgs p) {
             const int t0 = q.lo + i * kTile, buf = i & 1;
 #pragma unroll
             for (int k = 0; k < P::NV; ++k) {
-                const int t = (k * kFeed + tid) / P::VR;
+                const int t = (k * P::threads + tid) / kVR;
                 if (t0 + t < q.hi) {
-                    float xv[V], zv[V], out[V];
-                    unpack_raw<T>(x0[k], xv);
-                    unpack_raw<T>(z0[k], zv);
+                    float xv[kQ], zv[kQ], out[kQ];
+                    unpack_quad(x0[k], xv);
+                    unpack_quad(z0[k], zv);
 #pragma unroll
-                    for (int j = 0; j < V; ++j) {
-                        out[j] = fmaf(Dv[j], xv[j], YRow<T, NL>::sum(sm.y[buf][t], vc + j));
+                    for (int j = 0; j < kQ; ++j) {
+                        out[j] = fmaf(Dv[j], xv[j], YRow<NL>::sum(sm.y[buf][t], vc + j));
                         if (p.z) out[j] *= silu(zv[j]);
                     }
-                    st_vec<T>((T*)p.y + ((long long)q.sp.row * p.L + q.sp.first + t0 + t) * p.C + q.c0 + vc, out,
+                    st_quad<T>((T*)p.y + ((long long)q.sp.row * p.L + q.sp.first + t0 + t) * p.C + q.c0 + vc, out,
                               q.nc - vc, p.wide);
                 }
             }
@@ -362,6 +344,7 @@ __global__ void __launch_bounds__(32 * NL + kFeed) k_ssm_fwd(const SsmArgs p) {
     }
 
     // ---------------------------------------------------------------- scan
+    if constexpr (NL == 4) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kScanRegs4));
     const int lane = threadIdx.x & 31, nl = lane % NL;
     const int cl = (threadIdx.x >> 5) * (32 / NL) + lane / NL;    // channel within the block
     const bool cok = cl < q.nc;
@@ -397,6 +380,7 @@ __global__ void __launch_bounds__(32 * NL + kFeed) k_ssm_fwd(const SsmArgs p) {
             }
         }
     }
+    const f2 A01 = pack(A2[0], A2[1]), A23 = pack(A2[2], A2[3]);
     f2 h01 = pack(h[0], h[1]), h23 = pack(h[2], h[3]);
     const long long save0 = LOCAL ? 0 : save_slot(p, q.sp, q.s);
     float sum_d = 0.f;
@@ -405,12 +389,12 @@ __global__ void __launch_bounds__(32 * NL + kFeed) k_ssm_fwd(const SsmArgs p) {
         const int t0 = q.lo + i * kTile, buf = i & 1;
         // Operands of four tokens are fetched while the four before are worked on; the stores below would
         // otherwise hold back the loads behind them.
-        float2 dd[2][4];
+        f2 dd[2][4], dx[2][4];
         BC4<T> bc[2][4];
         auto fetch = [&](int t, int w) {
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
-                dd[w][u] = sm.dd[buf][t + u][DRow<T>::at(cl)];
+                ld_pairs((const float*)&sm.dd[buf][t + u][DRow::at(cl)], dd[w][u], dx[w][u]);
                 bc[w][u] = sm.bc[buf][t + u][nl];
             }
         };
@@ -425,18 +409,17 @@ __global__ void __launch_bounds__(32 * NL + kFeed) k_ssm_fwd(const SsmArgs p) {
             }
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
-                const float d = dd[w][u].x, dx = dd[w][u].y;
                 float b[4], cc[4];
                 if constexpr (LOCAL) get_b(bc[w][u], b);
                 else get_bc(bc[w][u], b, cc);
-                const f2 a01 = pack(ex2(d * A2[0]), ex2(d * A2[1])), a23 = pack(ex2(d * A2[2]), ex2(d * A2[3]));
-                h01 = fma2(a01, h01, pack(dx * b[0], dx * b[1]));
-                h23 = fma2(a23, h23, pack(dx * b[2], dx * b[3]));
+                const f2 a01 = ex2_2(mul2(dd[w][u], A01)), a23 = ex2_2(mul2(dd[w][u], A23));
+                h01 = fma2(a01, h01, mul2(dx[w][u], pack(b[0], b[1])));
+                h23 = fma2(a23, h23, mul2(dx[w][u], pack(b[2], b[3])));
                 if constexpr (LOCAL) {
-                    sum_d += d;
+                    sum_d += unpack(dd[w][u]).x;
                 } else {
                     const float2 s = unpack(fma2(h01, pack(cc[0], cc[1]), mul2(h23, pack(cc[2], cc[3]))));
-                    sm.y[buf][t + u][YRow<T, NL>::at(cl, nl)] = s.x + s.y;
+                    sm.y[buf][t + u][YRow<NL>::at(cl, nl)] = s.x + s.y;
                 }
             }
         }
@@ -459,12 +442,16 @@ __global__ void __launch_bounds__(32 * NL + kFeed) k_ssm_fwd(const SsmArgs p) {
 //   g_t = C_t r_t + a_{t+1} g_{t+1}
 //   dC_t = sum_c r_t h_t,  dB_t = sum_c g_t d_t x_t,  d(d x)_t = sum_n g_t B_t,
 //   e_t = a_t g_t h_{t-1},  dA = sum_t e_t d_t,  dd_t = sum_n e_t A + x_t d(d x)_t
-// The forward saved the state before every 16th token. From it 16 tokens are walked forward with
-// every a_t and h_t kept in registers, then walked back, so each exponential is made once.
+// The forward saved the state before every 16th token. From it 16 tokens are walked forward with every
+// h_t kept in registers, then walked back (their decays are formed again: kept too, they would leave
+// no registers for a second channel in each lane).
 //
-// Sums over the channels of a block: a lane's four states are held in an order that depends on the
-// lane's channel (slot j holds state j xor the channel's low bits), so halving the four slots over
-// the channel lanes needs no selects: what one lane gives away is what its partner keeps.
+// A block is four scanning warps and eight that feed them, as in the forward pass. A scanning lane has
+// two channels x four states: B and C, and the sums over channels for dB and dC, are then shared by
+// two. Those sums go over the warp's channel lanes by halving: what one lane gives away is what its
+// partner keeps. No selects are needed, since a lane holds its states in an order of its own (slot j is
+// state j xor the lane's low bits). The sums over n go the same way once (the two channels of
+// neighbouring lanes are in opposite order), and the feeding warps add the rest.
 constexpr int perm_copies(int NL) { return 32 / NL < 4 ? 32 / NL : 4; }
 
 __device__ __forceinline__ void permute4(float (&v)[4], int pm) {
@@ -478,18 +465,6 @@ __device__ __forceinline__ void permute4(float (&v)[4], int pm) {
     }
 }
 
-template <typename T, int NL> struct BwdSmem {
-    using P = Part<T, NL>;
-    static constexpr int PC = perm_copies(NL);
-    float2 dd[kTile][kCh];                 // d, d x
-    float r[kTile][kCh];                   // dy silu(z)
-    float B[kTile][PC][4 * NL], C[kTile][PC][4 * NL];
-    float o[3][kTile][kYS];                // sums over n: C h, g B, e A
-    float bc[NL][kSub][8 * NL];            // sums over a warp's channels: dB, dC
-    uint4 raw[4][P::vecs];                 // x, dt, z, dy of the tile
-    float acc[2][P::vecs < P::threads ? P::vecs : P::threads][P::V + 1];   // dD, d dt_bias of the thread's vector
-};
-
 // LOCAL: the first pass over pieces: what each piece passes back from a zero gradient behind it (all
 // pieces but the first) and its sum of steps.
 template <typename T, int NL>
@@ -498,7 +473,7 @@ __global__ void __launch_bounds__(32 * NL) k_ssm_bwd_local(const SsmArgs p) {
     constexpr int V = P::V;
     __shared__ __align__(16) float2 sdr[kTile][kCh];              // d, r
     __shared__ __align__(16) float sC[kTile][4 * NL];
-    const Place q = place_of(p, p.K - 1, 1);
+    const Place q = place_of(p, p.K - 1, 1, kCh, p.nb);
     const int lane = threadIdx.x & 31, nl = lane % NL;
     const int cl = (threadIdx.x >> 5) * (32 / NL) + lane / NL;
     const bool cok = cl < q.nc;
@@ -564,279 +539,414 @@ __global__ void __launch_bounds__(32 * NL) k_ssm_bwd_local(const SsmArgs p) {
     if (cok && nl == 0) p.sdt[slot * p.C + c] = sum_d;
 }
 
+constexpr int kScan = 128, kFeedB = 256, kTB = kSub;              // threads, tokens of a backward block's tile
+constexpr int kScanRegs = 248, kFeedRegs = 128;                   // 168 each at launch
+
+template <int NL> struct Bwd {
+    static constexpr int CH = 256 / NL;                           // channels of a block
+    static constexpr int QR = CH / kQ;                            // vectors of four channels in a token
+    static constexpr int quads = kTB * QR, NV = (quads + kFeedB - 1) / kFeedB, active = quads < kFeedB ? quads : kFeedB;
+    static constexpr int states = kTB * 4 * NL, NS = (states + kFeedB - 1) / kFeedB;
+    static constexpr int PC = perm_copies(NL), W = NL / 2;        // orders of B and C; shares of a sum over n
+};
+// Rows of pairs (d, d x), and of the shares of a sum over n: padded as in the forward pass.
+template <int NL> struct PRow {
+    static constexpr int vec = kQ + 2, len = Bwd<NL>::QR * vec;   // in pairs
+    static __device__ __forceinline__ int at(int c) { return c / kQ * vec + c % kQ; }
+};
+template <int NL> struct ORow {
+    static constexpr int W = Bwd<NL>::W, vec = kQ * W + 4, len = Bwd<NL>::QR * vec;
+    static __device__ __forceinline__ int at(int c, int w) { return c / kQ * vec + c % kQ * W + w; }
+    static __device__ __forceinline__ float sum(const float* row, int c) {
+        const float* s = row + at(c, 0);
+        float v = s[0];
+#pragma unroll
+        for (int k = 1; k < W; ++k) v += s[k];
+        return v;
+    }
+};
+
+template <typename T, int NL> struct BwdSmem {
+    float2 dd[2][kTB][PRow<NL>::len];
+    float r[2][kTB][Bwd<NL>::CH];                                 // dy silu(z)
+    BC4<T> bc[2][kTB][Bwd<NL>::PC][NL];
+    float o[2][3][kTB][ORow<NL>::len];                            // C h, g B, e A: shares of the sums over n
+    float sum[2][kScan / 32][kTB][8 * NL];                        // dB, dC: sums over a warp's channels
+};
+
 template <typename T, int NL>
-__global__ void __launch_bounds__(32 * NL) k_ssm_bwd(const SsmArgs p) {
-    using P = Part<T, NL>;
-    constexpr int V = P::V, PC = perm_copies(NL);
+__global__ void __launch_bounds__(kScan + kFeedB, 1) k_ssm_bwd(const SsmArgs p) {
+    using W = Bwd<NL>;
+    constexpr int PC = W::PC;
     constexpr unsigned all = 0xffffffffu;
     extern __shared__ __align__(16) unsigned char smem_raw[];
     BwdSmem<T, NL>& sm = *(BwdSmem<T, NL>*)smem_raw;
+    const Place q = place_of(p, p.K, 0, W::CH, p.nbb);
+    const int tiles = (q.hi - q.lo + kTB - 1) / kTB;
+    const long long slot = (long long)q.s * p.K + q.k;
 
-    const Place q = place_of(p, p.K, 0);
-    const int lane = threadIdx.x & 31, nl = lane % NL, warp = threadIdx.x >> 5;
-    const int ql = lane / NL, pm = ql & (PC - 1);                 // channel lane, order of the states
-    const int cl = warp * (32 / NL) + ql;
-    const bool cok = cl < q.nc;
-    const long long c = q.c0 + cl;
-    const int n0 = 4 * nl;
-    const bool keeps = cok && n0 < p.Np;
-
-    float A2[4], ag[4], dA[4] = {0.f, 0.f, 0.f, 0.f};
+    if (threadIdx.x >= kScan) {
+        // ------------------------------------------------------------ feed
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFeedRegs));
+        typedef typename Quad<T>::raw Raw;
+        const int tid = threadIdx.x - kScan;
+        const int vc = tid % W::QR * kQ;
+        float bias[kQ], Dv[kQ], sD[kQ], sb[kQ];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const bool ok = cok && n0 + j < p.N;
-        A2[j] = ok ? p.A[c * p.N + n0 + j] * kLog2e : 0.f;
-        ag[j] = ok && p.dh ? p.dh[((long long)q.s * p.C + c) * p.N + n0 + j] : 0.f;
-    }
-    if (keeps)
-        for (int k = p.K - 1; k > q.k; --k) {                     // join the pieces behind this one
-            const long long slot = (long long)q.s * p.K + k;
-            const float sd = p.sdt[slot * p.C + c];
-            const float4 m = *(const float4*)(p.loc + (slot * p.C + c) * p.Np + n0);
-            ag[0] = fmaf(ex2(sd * A2[0]), ag[0], m.x);
-            ag[1] = fmaf(ex2(sd * A2[1]), ag[1], m.y);
-            ag[2] = fmaf(ex2(sd * A2[2]), ag[2], m.z);
-            ag[3] = fmaf(ex2(sd * A2[3]), ag[3], m.w);
+        for (int j = 0; j < kQ; ++j) {
+            bias[j] = (p.bias && vc + j < q.nc) ? p.bias[q.c0 + vc + j] : 0.f;
+            Dv[j] = (p.D && vc + j < q.nc) ? p.D[q.c0 + vc + j] : 0.f;
+            sD[j] = sb[j] = 0.f;
         }
-    permute4(A2, pm);
-    permute4(ag, pm);
-
-    const int vc = threadIdx.x % P::VR * V;
-    const bool stages = threadIdx.x < P::vecs;
-    if (stages) {
+        // x, dt, z, dy: of the tile in flight, of the one staged last and of the one staged before it
+        Raw rr[4][W::NV], k1[4][W::NV], k0[4][W::NV];
+        T rB[W::NS], rC[W::NS];
+        auto load = [&](int i) {
+            if (i < 0) return;
+            const int t0 = q.lo + i * kTB;
+            auto one = [&](Raw (&r)[W::NV], const void* base, long long row, long long tok) {
 #pragma unroll
-        for (int j = 0; j < V; ++j) sm.acc[0][threadIdx.x][j] = sm.acc[1][threadIdx.x][j] = 0.f;
-    }
-    const long long save0 = save_slot(p, q.sp, q.s);
-    const int cbk = q.cb % p.nb;
-
-    uint4 rx[P::NV], rd[P::NV], rz[P::NV], rg[P::NV];
-    T rB[4], rC[4];
-    float4 rh[2];
-    auto load = [&](int t0) {
-        ld_part<T, NL>(rx, p.x, p.x_row, p.x_tok, q, t0, p.wide);
-        ld_part<T, NL>(rd, p.dt, p.dt_row, p.dt_tok, q, t0, p.wide);
-        ld_part<T, NL>(rg, p.dy, (long long)p.L * p.C, p.C, q, t0, p.wide);
-        if (p.z) ld_part<T, NL>(rz, p.z, p.z_row, p.z_tok, q, t0, p.wide);
-        ld_states<T, NL>(rB, p.Bm, p.b_row, p.b_tok, q, t0, threadIdx.x, p.N);
-        ld_states<T, NL>(rC, p.Cm, p.c_row, p.c_tok, q, t0, threadIdx.x, p.N);
+                for (int k = 0; k < W::NV; ++k) {
+                    const int v = k * kFeedB + tid, t = t0 + v / W::QR;
+                    r[k] = Raw{};
+                    if (v < W::quads && t < q.hi)
+                        r[k] = ld_quad((const T*)base + q.sp.row * row + (q.sp.first + t) * tok + q.c0 + vc, q.nc - vc, p.wide);
+                }
+            };
+            one(rr[0], p.x, p.x_row, p.x_tok);
+            one(rr[1], p.dt, p.dt_row, p.dt_tok);
+            if (p.z) one(rr[2], p.z, p.z_row, p.z_tok);
+            one(rr[3], p.dy, (long long)p.L * p.C, p.C);
 #pragma unroll
-        for (int s = 0; s < 2; ++s)
-            rh[s] = keeps && t0 + s * kSub < q.hi
-                        ? *(const float4*)(p.hsave + ((save0 + t0 / kSub + s) * p.C + c) * p.Np + n0)
-                        : make_float4(0.f, 0.f, 0.f, 0.f);
-    };
-    auto bias_of = [&](int j) { return p.bias && vc + j < q.nc ? __ldg(p.bias + q.c0 + vc + j) : 0.f; };
-
-    int t0 = q.lo + (q.hi - q.lo + kTile - 1) / kTile * kTile - kTile;
-    if (t0 >= q.lo) load(t0);
-    for (; t0 >= q.lo; t0 -= kTile) {
-#pragma unroll
-        for (int i = 0; i < P::NV; ++i) {
-            const int v = i * P::threads + threadIdx.x;
-            if (v < P::vecs) {
-                const int t = v / P::VR;
-                float xv[V], dv[V], zv[V], gv[V];
-                unpack_raw<T>(rx[i], xv);
-                unpack_raw<T>(rd[i], dv);
-                unpack_raw<T>(rz[i], zv);
-                unpack_raw<T>(rg[i], gv);
-                sm.raw[0][v] = rx[i];
-                sm.raw[1][v] = rd[i];
-                sm.raw[2][v] = rz[i];
-                sm.raw[3][v] = rg[i];
-                const bool ok = t0 + t < q.hi;
-#pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    float d = dv[j] + bias_of(j);
-                    if (p.softplus) d = softplus_of(d);
-                    d = ok && vc + j < q.nc ? d : 0.f;
-                    sm.dd[t][vc + j] = make_float2(d, ok ? d * xv[j] : 0.f);
-                    const float r = p.z ? gv[j] * silu(zv[j]) : gv[j];
-                    sm.r[t][vc + j] = ok ? r : 0.f;
+            for (int k = 0; k < W::NS; ++k) {
+                const int e = k * kFeedB + tid, t = t0 + e / (4 * NL), n = e % (4 * NL);
+                rB[k] = rC[k] = T(0.f);
+                if (e < W::states && t < q.hi && n < p.N) {
+                    rB[k] = ((const T*)p.Bm)[q.sp.row * p.b_row + (q.sp.first + t) * p.b_tok + (long long)q.g * p.N + n];
+                    rC[k] = ((const T*)p.Cm)[q.sp.row * p.c_row + (q.sp.first + t) * p.c_tok + (long long)q.g * p.N + n];
                 }
             }
-        }
+        };
+        auto stage = [&](int i) {
+            const int t0 = q.lo + i * kTB, buf = i & 1;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int e = i * P::threads + threadIdx.x;
-            const int t = e / (4 * NL), n = e % (4 * NL);
+            for (int k = 0; k < W::NV; ++k) {
+                const int v = k * kFeedB + tid, t = v / W::QR;
 #pragma unroll
-            for (int m = 0; m < PC; ++m) {
-                sm.B[t][m][n ^ m] = Io<T>::ld(&rB[i]);
-                sm.C[t][m][n ^ m] = Io<T>::ld(&rC[i]);
-            }
-        }
-        const float4 hin[2] = {rh[0], rh[1]};
-        __syncthreads();
-        if (t0 - kTile >= q.lo) load(t0 - kTile);
-
-#pragma unroll 1
-        for (int s = 1; s >= 0; --s) {
-            const int ts = s * kSub;
-            const float4 hf = s ? hin[1] : hin[0];
-            float hi4[4] = {hf.x, hf.y, hf.z, hf.w};
-            permute4(hi4, pm);
-            float a[kSub][4], h[kSub][4];
+                for (int m = 0; m < 4; ++m) { k0[m][k] = k1[m][k]; k1[m][k] = rr[m][k]; }
+                if (W::active == kFeedB || v < W::quads) {
+                    float xv[kQ], dv[kQ], zv[kQ], gv[kQ];
+                    unpack_quad(rr[0][k], xv);
+                    unpack_quad(rr[1][k], dv);
+                    unpack_quad(rr[2][k], zv);
+                    unpack_quad(rr[3][k], gv);
+                    const bool ok = t0 + t < q.hi;                // behind the end: no step; x and dy were read as zero
+                    float r[kQ];
 #pragma unroll
-            for (int i = 0; i < kSub; ++i) {
-                const float2 dd = sm.dd[ts + i][cl];
-                const float4 b = *(const float4*)&sm.B[ts + i][pm][n0];
-                const float bb[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    a[i][j] = ex2(dd.x * A2[j]);
-                    h[i][j] = fmaf(a[i][j], i ? h[i - 1][j] : hi4[j], dd.y * bb[j]);
-                }
-            }
-            float dAs[4] = {0.f, 0.f, 0.f, 0.f};                  // sums of 16 tokens join the long sum as one
-#pragma unroll
-            for (int i4 = kSub - 4; i4 >= 0; i4 -= 4) {
-                float yv[4], gv[4], ev[4];
-#pragma unroll
-                for (int u = 3; u >= 0; --u) {
-                    const int i = i4 + u;
-                    const float2 dd = sm.dd[ts + i][cl];
-                    const float r = sm.r[ts + i][cl];
-                    const float4 b = *(const float4*)&sm.B[ts + i][pm][n0];
-                    const float4 c4 = *(const float4*)&sm.C[ts + i][pm][n0];
-                    const float bb[4] = {b.x, b.y, b.z, b.w}, cc[4] = {c4.x, c4.y, c4.z, c4.w};
-                    float vB[4], vC[4];
-                    yv[u] = gv[u] = ev[u] = 0.f;
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const float g = fmaf(cc[j], r, ag[j]);
-                        vC[j] = r * h[i][j];
-                        vB[j] = g * dd.y;
-                        yv[u] = fmaf(cc[j], h[i][j], yv[u]);
-                        gv[u] = fmaf(g, bb[j], gv[u]);
-                        ag[j] = a[i][j] * g;
-                        const float e = ag[j] * (i ? h[i - 1][j] : hi4[j]);
-                        dAs[j] = fmaf(e, dd.x, dAs[j]);
-                        ev[u] = fmaf(e, A2[j], ev[u]);
+                    for (int j = 0; j < kQ; j += 2) {
+                        float2 d = make_float2(dv[j] + bias[j], dv[j + 1] + bias[j + 1]);
+                        if (p.softplus) d = softplus_of(d);
+                        if (!ok) d = make_float2(0.f, 0.f);
+                        const float2 w = unpack(mul2(pack(d.x, d.y), pack(xv[j], xv[j + 1])));
+                        *(float4*)&sm.dd[buf][t][PRow<NL>::at(vc + j)] = make_float4(d.x, w.x, d.y, w.y);
+                        r[j] = p.z ? gv[j] * silu(zv[j]) : gv[j];
+                        r[j + 1] = p.z ? gv[j + 1] * silu(zv[j + 1]) : gv[j + 1];
                     }
-                    // sums over the warp's channels
-                    vB[0] += __shfl_xor_sync(all, vB[1], NL);
-                    vB[2] += __shfl_xor_sync(all, vB[3], NL);
-                    vC[0] += __shfl_xor_sync(all, vC[1], NL);
-                    vC[2] += __shfl_xor_sync(all, vC[3], NL);
-                    float* out = sm.bc[warp][i];
-                    if constexpr (NL == 16) {
-                        out[n0 + pm] = vB[0];
-                        out[n0 + (2 ^ pm)] = vB[2];
-                        out[4 * NL + n0 + pm] = vC[0];
-                        out[4 * NL + n0 + (2 ^ pm)] = vC[2];
-                    } else {
-                        vB[0] += __shfl_xor_sync(all, vB[2], 2 * NL);
-                        vC[0] += __shfl_xor_sync(all, vC[2], 2 * NL);
-                        if constexpr (NL == 8) {
-                            out[n0 + pm] = vB[0];
-                            out[4 * NL + n0 + pm] = vC[0];
-                        } else {
-                            const bool up = ql & 4;
-                            float w = (up ? vC[0] : vB[0]) + __shfl_xor_sync(all, up ? vB[0] : vC[0], 4 * NL);
-                            if constexpr (NL == 2) w += __shfl_xor_sync(all, w, 8 * NL);
-                            if (NL != 2 || ql < 8) out[(up ? 4 * NL : 0) + n0 + pm] = w;
+                    *(float4*)&sm.r[buf][t][vc] = make_float4(r[0], r[1], r[2], r[3]);
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < W::NS; ++k) {
+                const int e = k * kFeedB + tid, t = e / (4 * NL), n = e % (4 * NL);
+                if (W::states >= kFeedB || e < W::states) {
+#pragma unroll
+                    for (int m = 0; m < PC; ++m) {
+                        T* to = sm.bc[buf][t][m][n / 4].v + (n % 4 ^ m);
+                        to[0] = rB[k];
+                        to[4] = rC[k];
+                    }
+                }
+            }
+        };
+        // Gradients of tile i (the one staged before the last) from the complete sums.
+        auto finish = [&](int i) {
+            const int t0 = q.lo + i * kTB, buf = i & 1;
+#pragma unroll
+            for (int k = 0; k < W::NV; ++k) {
+                const int v = k * kFeedB + tid, t = v / W::QR;
+                if (v < W::quads && t0 + t < q.hi) {
+                    float xv[kQ], dv[kQ], zv[kQ], gv[kQ], ox[kQ], od[kQ], oz[kQ];
+                    unpack_quad(k0[0][k], xv);
+                    unpack_quad(k0[1][k], dv);
+                    unpack_quad(k0[2][k], zv);
+                    unpack_quad(k0[3][k], gv);
+#pragma unroll
+                    for (int j = 0; j < kQ; ++j) {
+                        const float gB = ORow<NL>::sum(sm.o[buf][1][t], vc + j);
+                        const float eA = ORow<NL>::sum(sm.o[buf][2][t], vc + j) * kLn2;
+                        const float d = sm.dd[buf][t][PRow<NL>::at(vc + j)].x;
+                        float r = gv[j];
+                        if (p.z) {
+                            const float y = fmaf(Dv[j], xv[j], ORow<NL>::sum(sm.o[buf][0][t], vc + j));
+                            const float s = sigmoid(zv[j]);
+                            oz[j] = gv[j] * y * fmaf(zv[j] * s, 1.f - s, s);
+                            r *= zv[j] * s;
                         }
+                        ox[j] = fmaf(gB, d, Dv[j] * r);
+                        float w = fmaf(gB, xv[j], eA);
+                        if (p.softplus) w *= sigmoid(dv[j] + bias[j]);
+                        od[j] = w;
+                        sD[j] = fmaf(r, xv[j], sD[j]);
+                        sb[j] += w;
                     }
+                    const long long at = ((long long)q.sp.row * p.L + q.sp.first + t0 + t) * p.C + q.c0 + vc;
+                    st_quad<T>((T*)p.dx + at, ox, q.nc - vc, p.wide);
+                    st_quad<T>((T*)p.ddt + at, od, q.nc - vc, p.wide);
+                    if (p.z) st_quad<T>((T*)p.dz + at, oz, q.nc - vc, p.wide);
                 }
-                float w[2];
-                reduce_tokens<NL>(yv, nl, w);
-                put_tokens<NL>(&sm.o[0][ts + i4][0], cl, nl, w);
-                reduce_tokens<NL>(gv, nl, w);
-                put_tokens<NL>(&sm.o[1][ts + i4][0], cl, nl, w);
-                reduce_tokens<NL>(ev, nl, w);
-                put_tokens<NL>(&sm.o[2][ts + i4][0], cl, nl, w);
             }
+            // the warps' sums in order, to this block's part of dB and dC
 #pragma unroll
-            for (int j = 0; j < 4; ++j) dA[j] += dAs[j];
-            __syncthreads();
-            // sums over the warps, to this block's part of dB and dC
-            for (int e = threadIdx.x; e < kSub * 8 * NL; e += P::threads) {
-                const int i = e / (8 * NL), v = e % (8 * NL);
+            for (int k = 0; k < kTB * 8 * NL / kFeedB; ++k) {
+                const int e = k * kFeedB + tid, t = e / (8 * NL), v = e % (8 * NL);
                 float w = 0.f;
 #pragma unroll
-                for (int k = 0; k < NL; ++k) w += sm.bc[k][i][v];
-                const int t = t0 + ts + i;
-                if (t < q.hi)
-                    p.dbc_part[(((long long)cbk * p.B * p.L + (long long)q.sp.row * p.L + q.sp.first + t) * p.G + q.g) *
-                                   (8 * NL) + v] = w;
+                for (int m = 0; m < kScan / 32; ++m) w += sm.sum[buf][m][t][v];
+                if (t0 + t < q.hi)
+                    p.dbc_part[(((long long)(q.cb % p.nbb) * p.B * p.L + (long long)q.sp.row * p.L + q.sp.first + t0 + t) *
+                                    p.G + q.g) * (8 * NL) + v] = w;
             }
-            if (s == 1) __syncthreads();
+        };
+        if (tiles > 0) {
+            load(tiles - 1);
+            stage(tiles - 1);
+            load(tiles - 2);
         }
-        // per (t, c): the gradients of x, dt, z
-#pragma unroll
-        for (int i = 0; i < P::NV; ++i) {
-            const int v = i * P::threads + threadIdx.x;
-            const int t = v / P::VR;
-            if (v < P::vecs && t0 + t < q.hi) {
-                float xv[V], dv[V], zv[V], gv[V], ox[V], od[V], oz[V];
-                unpack_raw<T>(sm.raw[0][v], xv);
-                unpack_raw<T>(sm.raw[1][v], dv);
-                unpack_raw<T>(sm.raw[2][v], zv);
-                unpack_raw<T>(sm.raw[3][v], gv);
-#pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    const float Dj = p.D && vc + j < q.nc ? __ldg(p.D + q.c0 + vc + j) : 0.f;
-                    const float r = sm.r[t][vc + j], d = sm.dd[t][vc + j].x;
-                    const float gB = sm.o[1][t][vc + j], eA = sm.o[2][t][vc + j] * kLn2;
-                    ox[j] = fmaf(gB, d, Dj * r);
-                    float w = fmaf(gB, xv[j], eA);
-                    if (p.softplus) w *= sigmoid(dv[j] + bias_of(j));
-                    od[j] = w;
-                    if (p.z) oz[j] = gv[j] * fmaf(Dj, xv[j], sm.o[0][t][vc + j]) * silu_slope(zv[j]);
-                    sm.acc[0][threadIdx.x][j] = fmaf(r, xv[j], sm.acc[0][threadIdx.x][j]);
-                    sm.acc[1][threadIdx.x][j] += w;
-                }
-                const long long at = ((long long)q.sp.row * p.L + q.sp.first + t0 + t) * p.C + q.c0 + vc;
-                st_vec<T>((T*)p.dx + at, ox, q.nc - vc, p.wide);
-                st_vec<T>((T*)p.ddt + at, od, q.nc - vc, p.wide);
-                if (p.z) st_vec<T>((T*)p.dz + at, oz, q.nc - vc, p.wide);
-            }
-        }
-        // the staging of the next tile overwrites what other threads still read here: r and dd are read by
-        // their own writer only, o by the epilogue above, B and C in the walks behind a barrier each
         __syncthreads();
+        for (int i = tiles - 1; i >= 0; --i) {
+            if (i > 0) {
+                stage(i - 1);
+                load(i - 2);
+            } else {
+#pragma unroll
+                for (int k = 0; k < W::NV; ++k)
+#pragma unroll
+                    for (int m = 0; m < 4; ++m) k0[m][k] = k1[m][k];
+            }
+            __syncthreads();
+            finish(i);                                            // d of tile i is overwritten behind the next barrier only
+        }
+        // dD and d dt_bias: the threads that share a vector of channels, in order
+        asm volatile("bar.sync 1, 256;" ::: "memory");
+        float* acc = &sm.o[0][0][0][0];
+        static_assert(sizeof(sm.o) >= kFeedB * 2 * kQ * sizeof(float), "the sums fit where the shares were");
+#pragma unroll
+        for (int j = 0; j < kQ; ++j) {
+            acc[tid * 2 * kQ + j] = sD[j];
+            acc[tid * 2 * kQ + kQ + j] = sb[j];
+        }
+        asm volatile("bar.sync 1, 256;" ::: "memory");
+        for (int e = tid; e < 2 * W::CH; e += kFeedB) {
+            const int which = e / W::CH, cc = e % W::CH;
+            float w = 0.f;
+            for (int i = cc / kQ; i < W::active; i += W::QR) w += acc[i * 2 * kQ + which * kQ + cc % kQ];
+            if (cc < q.nc) p.dch_part[(slot * 2 + which) * p.C + q.c0 + cc] = w;
+        }
+        return;
     }
 
-    permute4(ag, pm);
-    permute4(dA, pm);
-    const long long slot = (long long)q.s * p.K + q.k;
-    if (keeps) *(float4*)(p.dA_part + (slot * p.C + c) * p.Np + n0) = make_float4(dA[0], dA[1], dA[2], dA[3]);
-    if (p.dh0 && q.k == 0) {
+    // ---------------------------------------------------------------- scan
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kScanRegs));
+    const int lane = threadIdx.x & 31, nl = lane % NL, warp = threadIdx.x >> 5;
+    const int ql = lane / NL, pm = ql & (PC - 1);                 // channel lane, order of the states
+    const int b = nl & 1;
+    // slot 0 is the channel whose sums over n this lane keeps, slot 1 the one it gives to its neighbour
+    const int cl[2] = {warp * (64 / NL) + 2 * ql + b, warp * (64 / NL) + 2 * ql + 1 - b};
+    const int n0 = 4 * nl;
+    bool keeps[2];
+    float A[2][4], ag4[2][4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            if (cok && n0 + j < p.N) p.dh0[((long long)q.s * p.C + c) * p.N + n0 + j] = ag[j];
+    for (int s = 0; s < 2; ++s) {
+        const bool cok = cl[s] < q.nc;
+        const long long c = q.c0 + cl[s];
+        keeps[s] = cok && n0 < p.Np;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const bool ok = cok && n0 + j < p.N;
+            A[s][j] = ok ? p.A[c * p.N + n0 + j] * kLog2e : 0.f;
+            ag4[s][j] = ok && p.dh ? p.dh[((long long)q.s * p.C + c) * p.N + n0 + j] : 0.f;
+        }
+        if (keeps[s])
+            for (int k = p.K - 1; k > q.k; --k) {                 // join the pieces behind this one
+                const long long sl = (long long)q.s * p.K + k;
+                const float sd = p.sdt[sl * p.C + c];
+                const float4 m = *(const float4*)(p.loc + (sl * p.C + c) * p.Np + n0);
+                ag4[s][0] = fmaf(ex2(sd * A[s][0]), ag4[s][0], m.x);
+                ag4[s][1] = fmaf(ex2(sd * A[s][1]), ag4[s][1], m.y);
+                ag4[s][2] = fmaf(ex2(sd * A[s][2]), ag4[s][2], m.z);
+                ag4[s][3] = fmaf(ex2(sd * A[s][3]), ag4[s][3], m.w);
+            }
+        permute4(A[s], pm);
+        permute4(ag4[s], pm);
     }
-    __syncthreads();
-    constexpr int TL = (P::vecs < P::threads ? P::vecs : P::threads) / P::VR;   // threads that share a vector
-    if (threadIdx.x < 2 * kCh) {
-        const int which = threadIdx.x / kCh, cc = threadIdx.x % kCh;
-        float w = 0.f;
+    f2 A2[2][2], ag[2][2], dA[2][2];
 #pragma unroll
-        for (int i = 0; i < TL; ++i) w += sm.acc[which][i * P::VR + cc / V][cc % V];
-        if (cc < q.nc) p.dch_part[(slot * 2 + which) * p.C + q.c0 + cc] = w;
+    for (int s = 0; s < 2; ++s)
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+            A2[s][m] = pack(A[s][2 * m], A[s][2 * m + 1]);
+            ag[s][m] = pack(ag4[s][2 * m], ag4[s][2 * m + 1]);
+            dA[s][m] = pack(0.f, 0.f);
+        }
+    const long long save0 = save_slot(p, q.sp, q.s);
+    float4 rh[2];
+    auto load_h = [&](int i) {
+        if (i < 0) return;
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+            rh[s] = keeps[s] ? *(const float4*)(p.hsave + ((save0 + q.lo / kSub + i) * p.C + q.c0 + cl[s]) * p.Np + n0)
+                             : make_float4(0.f, 0.f, 0.f, 0.f);
+    };
+    load_h(tiles - 1);
+    __syncthreads();
+    for (int i = tiles - 1; i >= 0; --i) {
+        const int buf = i & 1;
+        f2 hin[2][2], h[kTB][2][2];
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            float f[4] = {rh[s].x, rh[s].y, rh[s].z, rh[s].w};
+            permute4(f, pm);
+            hin[s][0] = pack(f[0], f[1]);
+            hin[s][1] = pack(f[2], f[3]);
+        }
+        load_h(i - 1);
+#pragma unroll
+        for (int t = 0; t < kTB; ++t) {
+            float bb[4];
+            get_b(sm.bc[buf][t][pm][nl], bb);
+            const f2 b01 = pack(bb[0], bb[1]), b23 = pack(bb[2], bb[3]);
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                const float2 dd = sm.dd[buf][t][PRow<NL>::at(cl[s])];
+                const f2 d = both(dd.x), dx = both(dd.y);
+                h[t][s][0] = fma2(ex2_2(mul2(d, A2[s][0])), t ? h[t - 1][s][0] : hin[s][0], mul2(dx, b01));
+                h[t][s][1] = fma2(ex2_2(mul2(d, A2[s][1])), t ? h[t - 1][s][1] : hin[s][1], mul2(dx, b23));
+            }
+        }
+        f2 dAs[2][2];                                             // sums of 16 tokens join the long sum as one
+#pragma unroll
+        for (int s = 0; s < 2; ++s) dAs[s][0] = dAs[s][1] = pack(0.f, 0.f);
+#pragma unroll
+        for (int t = kTB - 1; t >= 0; --t) {
+            float bb[4], cc[4];
+            get_bc(sm.bc[buf][t][pm][nl], bb, cc);
+            const f2 b2[2] = {pack(bb[0], bb[1]), pack(bb[2], bb[3])}, c2[2] = {pack(cc[0], cc[1]), pack(cc[2], cc[3])};
+            f2 vB[2], vC[2];
+            float yv[2], gv[2], ev[2];
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                const float2 dd = sm.dd[buf][t][PRow<NL>::at(cl[s])];
+                const f2 d = both(dd.x), dx = both(dd.y), r = both(sm.r[buf][t][cl[s]]);
+                f2 y, gb, ea;
+#pragma unroll
+                for (int m = 0; m < 2; ++m) {
+                    const f2 hp = t ? h[t - 1][s][m] : hin[s][m];
+                    const f2 g = fma2(c2[m], r, ag[s][m]);
+                    vC[m] = s ? fma2(r, h[t][s][m], vC[m]) : mul2(r, h[t][s][m]);
+                    vB[m] = s ? fma2(g, dx, vB[m]) : mul2(g, dx);
+                    y = m ? fma2(c2[m], h[t][s][m], y) : mul2(c2[m], h[t][s][m]);
+                    gb = m ? fma2(g, b2[m], gb) : mul2(g, b2[m]);
+                    ag[s][m] = mul2(ex2_2(mul2(d, A2[s][m])), g);
+                    const f2 e = mul2(ag[s][m], hp);
+                    dAs[s][m] = fma2(e, d, dAs[s][m]);
+                    ea = m ? fma2(e, A2[s][m], ea) : mul2(e, A2[s][m]);
+                }
+                const float2 u = unpack(y), v = unpack(gb), w = unpack(ea);
+                yv[s] = u.x + u.y;
+                gv[s] = v.x + v.y;
+                ev[s] = w.x + w.y;
+            }
+            // slot 1 is the neighbour's slot 0
+            const int oc = ORow<NL>::at(cl[0], nl >> 1);
+            sm.o[buf][0][t][oc] = yv[0] + __shfl_xor_sync(all, yv[1], 1);
+            sm.o[buf][1][t][oc] = gv[0] + __shfl_xor_sync(all, gv[1], 1);
+            sm.o[buf][2][t][oc] = ev[0] + __shfl_xor_sync(all, ev[1], 1);
+            // sums over the warp's channels
+            float* out = sm.sum[buf][warp][t];
+            const float2 B0 = unpack(vB[0]), B1 = unpack(vB[1]), C0 = unpack(vC[0]), C1 = unpack(vC[1]);
+            float vb = B0.x + __shfl_xor_sync(all, B0.y, NL), vb2 = B1.x + __shfl_xor_sync(all, B1.y, NL);
+            float vc = C0.x + __shfl_xor_sync(all, C0.y, NL), vc2 = C1.x + __shfl_xor_sync(all, C1.y, NL);
+            if constexpr (NL == 16) {
+                out[n0 + pm] = vb;
+                out[n0 + (2 ^ pm)] = vb2;
+                out[4 * NL + n0 + pm] = vc;
+                out[4 * NL + n0 + (2 ^ pm)] = vc2;
+            } else {
+                vb += __shfl_xor_sync(all, vb2, 2 * NL);
+                vc += __shfl_xor_sync(all, vc2, 2 * NL);
+                if constexpr (NL == 8) {
+                    out[n0 + pm] = vb;
+                    out[4 * NL + n0 + pm] = vc;
+                } else {
+                    const bool up = ql & 4;
+                    float w = (up ? vc : vb) + __shfl_xor_sync(all, up ? vb : vc, 4 * NL);
+                    if constexpr (NL == 2) w += __shfl_xor_sync(all, w, 8 * NL);
+                    if (NL != 2 || ql < 8) out[(up ? 4 * NL : 0) + n0 + pm] = w;
+                }
+            }
+        }
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+            for (int m = 0; m < 2; ++m) dA[s][m] = add2(dA[s][m], dAs[s][m]);
+        __syncthreads();
+    }
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+        const long long c = q.c0 + cl[s];
+        const float2 u = unpack(ag[s][0]), v = unpack(ag[s][1]), x = unpack(dA[s][0]), y = unpack(dA[s][1]);
+        float f[4] = {u.x, u.y, v.x, v.y}, a[4] = {x.x, x.y, y.x, y.y};
+        permute4(f, pm);
+        permute4(a, pm);
+        if (keeps[s]) *(float4*)(p.dA_part + (slot * p.C + c) * p.Np + n0) = make_float4(a[0], a[1], a[2], a[3]);
+        if (p.dh0 && q.k == 0) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (cl[s] < q.nc && n0 + j < p.N) p.dh0[((long long)q.s * p.C + c) * p.N + n0 + j] = f[j];
+        }
     }
 }
 
-// dB and dC: the channel blocks of a group in order. Thread = (token, group, B or C, state).
+// dB and dC: the channel blocks of a group in order. Thread = four of a token's values (w4 such fours,
+// B's before C's).
 template <typename T>
-__global__ void k_ssm_sum_bc(const float* part, const int* cu, int S, int B, int L, int G, int N, int nb, int w8,
+__global__ void k_ssm_sum_bc(const float* part, const int* cu, int S, int B, int L, int G, int N, int nb, int w4,
                              T* dBm, T* dCm) {
-    const long long per = (long long)B * L * G * w8;
+    const long long per = (long long)B * L * G * w4;
     const long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x;
     if (i >= per) return;
-    const int v = (int)(i % w8);
-    const long long tg = i / w8;                                   // token * G + group
+    const int v = (int)(i % w4);
+    const long long tg = i / w4;                                   // token * G + group
     if (cu) {
         const long long t = tg / G;
         if (t < min(max(cu[0], 0), L) || t >= min(max(cu[S], 0), L)) return;
     }
-    const int n = v % (w8 / 2);
+    const int n = v % (w4 / 2) * 4;
     if (n >= N) return;
-    float w = 0.f;
-    for (int k = 0; k < nb; ++k) w += part[k * per + i];
-    Io<T>::st((v < w8 / 2 ? dBm : dCm) + tg * N + n, w);
+    const float4* s = (const float4*)part + i;
+    f2 a = pack(0.f, 0.f), b = a;
+#pragma unroll 8
+    for (int k = 0; k < nb; ++k) {
+        const float4 f = s[k * per];
+        a = add2(a, pack(f.x, f.y));
+        b = add2(b, pack(f.z, f.w));
+    }
+    const float2 x = unpack(a), y = unpack(b);
+    const float o[4] = {x.x, x.y, y.x, y.y};
+    T* to = (v < w4 / 2 ? dBm : dCm) + tg * N + n;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        if (n + j < N) Io<T>::st(to + j, o[j]);
 }
 
 // dA, dD, d dt_bias: the sequences' pieces in order.
@@ -932,6 +1042,8 @@ __global__ void k_ssm_step(const SsmArgs p, const int* idx, int slots, int NL) {
 }
 
 // ---------------------------------------------------------------------------------------- host
+constexpr size_t kHalfSmem = 116 * 1024;
+
 int lanes_for(int N) { return N <= 8 ? 2 : N <= 16 ? 4 : N <= 32 ? 8 : 16; }
 
 bool make_args(const gspn_ssm_desc* d, SsmArgs* p) {
@@ -948,6 +1060,7 @@ bool make_args(const gspn_ssm_desc* d, SsmArgs* p) {
     p->S = d->S > 0 ? d->S : d->B;
     p->Np = (d->N + 3) / 4 * 4;
     p->nb = (d->C / d->G + kCh - 1) / kCh;
+    p->nbb = (d->C / d->G + 256 / lanes_for(d->N) - 1) / (256 / lanes_for(d->N));
     p->softplus = d->softplus;
     p->x_row = d->x_row; p->x_tok = d->x_tok; p->dt_row = d->dt_row; p->dt_tok = d->dt_tok;
     p->z_row = d->z_row; p->z_tok = d->z_tok; p->b_row = d->b_row; p->b_tok = d->b_tok;
@@ -960,17 +1073,29 @@ bool fits(const SsmArgs& p) {
            (long long)p.S * p.nb * p.G * 64 < (1LL << 31);
 }
 
-// Pieces of a sequence. Whole sequences are walked where their blocks fill half of the SMs: pieces
-// make every exponential twice, so they have to bring more than twice the blocks.
+// Pieces of a sequence. A block that has an SM to itself takes 81 cycles a token, two that share it 132,
+// and the first pass over pieces costs 0.6 of the main one (bf16, N = 16), so pieces pay where whole
+// sequences fill less than 3/4 of the SMs. Then as many as fit two to an SM at once, of 64 tokens at
+// least.
 int pieces_for(const SsmArgs& p, int sms) {
     const long long blocks = (long long)p.S * p.nb * p.G;
     const long long len = p.S > 0 && p.cu ? p.L / p.S : p.L;
-    if (2 * blocks >= sms) return 1;
-    long long K = (2LL * sms + blocks - 1) / blocks;
+    if (4 * blocks >= 3LL * sms) return 1;
+    long long K = 2LL * sms / blocks;
     K = K < 64 ? K : 64;
     const long long most = len / 64;
     K = K < most ? K : most;
-    return K < 3 ? 1 : (int)K;
+    return K < 2 ? 1 : (int)K;
+}
+
+// The warps that scan take over registers of the ones that feed (setmaxnreg): the two shares have to be
+// what the block was launched with, or the taking warps would wait for good.
+template <typename K>
+cudaError_t check_registers(K kernel, int threads, int needed) {
+    cudaFuncAttributes a;
+    const cudaError_t e = cudaFuncGetAttributes(&a, kernel);
+    if (e != cudaSuccess) return e;
+    return a.numRegs * threads >= needed ? cudaSuccess : cudaErrorInvalidKernelImage;
 }
 
 struct Carve {
@@ -992,7 +1117,7 @@ Carve carve(const SsmArgs& p, bool bwd) {
     if (bwd) {
         w.dA = take((size_t)p.S * p.K * CN);
         w.dch = take((size_t)p.S * p.K * 2 * p.C);
-        w.dbc = take((size_t)p.nb * p.B * p.L * p.G * 8 * lanes_for(p.N));
+        w.dbc = take((size_t)p.nbb * p.B * p.L * p.G * 8 * lanes_for(p.N));
     }
     w.total = off;
     return w;
@@ -1070,8 +1195,16 @@ gspn_status gspn_ssm_forward(const gspn_ssm_desc* desc, const void* x, const voi
         constexpr int NL = decltype(nl)::value;
         const unsigned cblocks = p.nb * p.G;
         auto go = [&](auto kernel, size_t smem, unsigned pieces) {
+            // Fewer blocks than SMs should have one SM each, but two of them fit on one and some would share it:
+            // ask for more shared memory than half of an SM's.
+            const unsigned blocks = cblocks * pieces * p.S;
+            if (blocks <= (unsigned)device_sm_count() && smem < kHalfSmem) smem = kHalfSmem;
+            if (NL == 4) {
+                static const cudaError_t regs = check_registers(kernel, kFwdThreads4, kFwdRegs4);
+                if (e == cudaSuccess) e = regs;
+            }
             if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-            if (e == cudaSuccess) kernel<<<cblocks * pieces * p.S, 32 * NL + kFeed, smem, st>>>(p);
+            if (e == cudaSuccess) kernel<<<blocks, 32 * NL + Feed<NL>::threads, smem, st>>>(p);
         };
         if (p.K > 1) go(k_ssm_fwd<T, NL, true>, sizeof(FwdSmem<T, NL, true>), p.K - 1);
         go(k_ssm_fwd<T, NL, false>, sizeof(FwdSmem<T, NL, false>), p.K);
@@ -1117,14 +1250,17 @@ gspn_status gspn_ssm_backward(const gspn_ssm_desc* desc, const void* x, const vo
         constexpr int NL = decltype(nl)::value;
         const unsigned cblocks = p.nb * p.G;
         const size_t smem = sizeof(BwdSmem<T, NL>);
+        static const cudaError_t regs = check_registers(k_ssm_bwd<T, NL>, kScan + kFeedB, kScan * kScanRegs + kFeedB * kFeedRegs);
+        e = regs;
+        if (e != cudaSuccess) return;
         e = cudaFuncSetAttribute(k_ssm_bwd<T, NL>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e != cudaSuccess) return;
         if (p.K > 1) k_ssm_bwd_local<T, NL><<<cblocks * (p.K - 1) * p.S, 32 * NL, 0, st>>>(p);
-        k_ssm_bwd<T, NL><<<cblocks * p.K * p.S, 32 * NL, smem, st>>>(p);
-        const long long per = (long long)p.B * p.L * p.G * 8 * NL;
-        if (per > 0)
-            k_ssm_sum_bc<T><<<(unsigned)((per + 255) / 256), 256, 0, st>>>(p.dbc_part, cu, p.S, p.B, p.L, p.G, p.N, p.nb,
-                                                                         8 * NL, (T*)dBm, (T*)dCm);
+        k_ssm_bwd<T, NL><<<(unsigned)(p.nbb * p.G) * p.K * p.S, kScan + kFeedB, smem, st>>>(p);
+        const long long quads = (long long)p.B * p.L * p.G * 2 * NL;
+        if (quads > 0)
+            k_ssm_sum_bc<T><<<(unsigned)((quads + 127) / 128), 128, 0, st>>>(p.dbc_part, cu, p.S, p.B, p.L, p.G, p.N, p.nbb,
+                                                                           2 * NL, (T*)dBm, (T*)dCm);
         const long long na = (long long)p.C * p.Np + 2 * p.C;
         k_ssm_sum_ac<<<(unsigned)((na + 255) / 256), 256, 0, st>>>(p.dA_part, p.dch_part, p.S * p.K, p.C, p.N, p.Np, dA,
                                                                   dD, ddt_bias);

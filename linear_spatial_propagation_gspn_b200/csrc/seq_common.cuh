@@ -61,6 +61,36 @@ __device__ __forceinline__ void st_vec(T* p, const float (&v)[Vec<T>::V], int n,
     }
 }
 
+// Four consecutive elements, as stored.
+template <typename T> struct Quad;
+template <> struct Quad<float> { typedef uint4 raw; };
+template <> struct Quad<__nv_bfloat16> { typedef uint2 raw; };
+
+__device__ __forceinline__ uint4 ld_quad(const float* p, int n, bool wide) { return ld_raw<float>(p, n, wide); }
+__device__ __forceinline__ uint2 ld_quad(const __nv_bfloat16* p, int n, bool wide) {
+    if (wide && n >= 4) return *(const uint2*)p;
+    const uint16_t* s = (const uint16_t*)p;
+    auto two = [&](int i) { return (n > i ? (uint32_t)s[i] : 0u) | (n > i + 1 ? (uint32_t)s[i + 1] << 16 : 0u); };
+    return make_uint2(two(0), two(2));
+}
+__device__ __forceinline__ void unpack_quad(const uint4& q, float (&v)[4]) {
+    v[0] = __uint_as_float(q.x); v[1] = __uint_as_float(q.y); v[2] = __uint_as_float(q.z); v[3] = __uint_as_float(q.w);
+}
+__device__ __forceinline__ void unpack_quad(const uint2& q, float (&v)[4]) {
+    v[0] = __uint_as_float(q.x << 16); v[1] = __uint_as_float(q.x & 0xffff0000u);
+    v[2] = __uint_as_float(q.y << 16); v[3] = __uint_as_float(q.y & 0xffff0000u);
+}
+template <typename T>
+__device__ __forceinline__ void st_quad(T* p, const float (&v)[4], int n, bool wide) {
+    if (wide && n >= 4) {
+        st_lanes<T, 4>(p, v);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (i < n) Io<T>::st(p + i, v[i]);
+    }
+}
+
 // ------------------------------------------------------------------ functions
 __device__ __forceinline__ float ex2(float v) {
     float r;
@@ -118,6 +148,13 @@ __device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
 __device__ __forceinline__ f2 ex2_2(f2 v) {
     const float2 s = unpack(v);
     return pack(ex2(s.x), ex2(s.y));
+}
+__device__ __forceinline__ f2 both(float v) { return pack(v, v); }
+// The larger of the two, NaN if either is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
 }
 // Four floats of shared memory (16-byte aligned) as two pairs.
 __device__ __forceinline__ void ld_pairs(const float* p, f2& a, f2& b) {
