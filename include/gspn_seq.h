@@ -45,8 +45,7 @@ typedef struct {
 GSPN_API size_t gspn_conv_workspace_size(const gspn_conv_desc *desc, int for_backward);
 
 /* y: B x L x C. state (S or B x K-1 x C, storage dtype, or null) receives the last K-1 inputs of
- * every sequence; it may be state0 itself only if the two are the same buffer of a call with L = 0
- * tokens, otherwise they must not overlap. */
+ * every sequence; it may be state0 itself, and must not overlap it otherwise. */
 GSPN_API gspn_status gspn_conv_forward(const gspn_conv_desc *desc, const void *x, const float *w,
                                        const float *bias, const int *cu, const void *state0, void *y,
                                        void *state, void *stream);

@@ -17,7 +17,7 @@ constexpr int kBatch = 4;       // tokens whose loads are in flight together
 
 struct ConvArgs {
     int B, L, C, S, silu;
-    bool wide;
+    bool wide, wide_w;          // 16-byte aligned vectors of channels; of filters
     const void* x;
     long long x_row, x_tok;
     const float *w, *bias;
@@ -72,35 +72,70 @@ __device__ __forceinline__ Seq find(const ConvArgs& p, int row, int t) {
     return s;
 }
 
+// Loads of `P` pairs of channels (n of them exist): as stored, and taken apart.
+template <typename T, int P> struct Raw { typedef uint4 type; };
+template <> struct Raw<__nv_bfloat16, 2> { typedef uint2 type; };
+template <typename T, int P>
+__device__ __forceinline__ typename Raw<T, P>::type ld_pairs_raw(const T* p, int n, bool wide) {
+    if constexpr (2 * P == Vec<T>::V) return ld_raw<T>(p, n, wide);
+    else return ld_quad(p, n, wide);
+}
+template <typename T, int P>
+__device__ __forceinline__ void st_pairs(T* p, const f2 (&v)[P], int n, bool wide) {
+    float f[2 * P];
+    to_floats(v, f);
+    st_ch<T, 2 * P>(p, f, n, wide);
+}
+
 // The K - 1 inputs before token t of sequence s.
-template <typename T, int K, int L>
-__device__ __forceinline__ void window(const ConvArgs& p, const T* xr, const Seq& s, int t, int c, int n,
-                                       float (&win)[K][L]) {
+template <typename T, int K, int P>
+__device__ __forceinline__ void window(const ConvArgs& p, const T* xr, const Seq& s, int t, int c, int n, f2 (&win)[K][P]) {
 #pragma unroll
     for (int j = 0; j < K - 1; ++j) {
         const int at = t - (K - 1) + j;
-#pragma unroll
-        for (int i = 0; i < L; ++i) win[j][i] = 0.f;
-        if (at >= s.start) ld_ch<T, L>(xr + at * p.x_tok, win[j], n, p.wide);
+        typename Raw<T, P>::type q{};
+        if (at >= s.start) q = ld_pairs_raw<T, P>(xr + at * p.x_tok, n, p.wide);
         else if (p.state0)
-            ld_ch<T, L>((const T*)p.state0 + ((long long)s.q * (K - 1) + (K - 1 + at - s.start)) * p.C + c, win[j], n,
-                        p.wide);
+            q = ld_pairs_raw<T, P>((const T*)p.state0 + ((long long)s.q * (K - 1) + (K - 1 + at - s.start)) * p.C + c, n, p.wide);
+        to_pairs(q, win[j]);
     }
 }
 
-template <int K, int L>
-__device__ __forceinline__ void load_taps(const ConvArgs& p, int c, int n, float (&w)[K][L], float (&b)[L]) {
+// A thread's filters: 2 P K consecutive floats.
+template <int K, int P>
+__device__ __forceinline__ void load_taps(const ConvArgs& p, int c, int n, f2 (&w)[K][P], f2 (&b)[P]) {
+    float f[2 * P * K], bb[2 * P];
+    const float* s = p.w + (long long)c * K;
+    if (p.wide_w && n >= 2 * P) {
 #pragma unroll
-    for (int i = 0; i < L; ++i) {
+        for (int i = 0; i < 2 * P * K; i += 4) {
+            const float4 v = *(const float4*)(s + i);
+            f[i] = v.x; f[i + 1] = v.y; f[i + 2] = v.z; f[i + 3] = v.w;
+        }
+    } else {
 #pragma unroll
-        for (int k = 0; k < K; ++k) w[k][i] = i < n ? p.w[(long long)(c + i) * K + k] : 0.f;
-        b[i] = i < n && p.bias ? p.bias[c + i] : 0.f;
+        for (int i = 0; i < 2 * P * K; ++i) f[i] = i / K < n ? s[i] : 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < 2 * P; ++i) bb[i] = i < n && p.bias ? p.bias[c + i] : 0.f;
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+        b[i] = pack(bb[2 * i], bb[2 * i + 1]);
+#pragma unroll
+        for (int k = 0; k < K; ++k) w[k][i] = pack(f[2 * i * K + k], f[(2 * i + 1) * K + k]);
     }
 }
 
+template <typename T, int K> __device__ void last_inputs(const ConvArgs& p, long long id);
+
+// Blocks behind the first `tokens` take the states behind the sequences.
 template <typename T, int K>
-__global__ void __launch_bounds__(128) k_conv_fwd(const ConvArgs p) {
-    constexpr int V = Vec<T>::V;
+__global__ void __launch_bounds__(128) k_conv_fwd(const ConvArgs p, long long blocks) {
+    constexpr int V = Vec<T>::V, P = V / 2;
+    if (blockIdx.x >= blocks) {
+        last_inputs<T, K>(p, (blockIdx.x - blocks) * (long long)blockDim.x + threadIdx.x);
+        return;
+    }
     const long long id = (long long)blockIdx.x * blockDim.x + threadIdx.x;
     const int cv = (int)(id % p.nvec);
     const long long rr = id / p.nvec;
@@ -111,46 +146,60 @@ __global__ void __launch_bounds__(128) k_conv_fwd(const ConvArgs p) {
     const int c = cv * V, n = p.C - c;
     if (p.cu) t = max(t, cu_at(p, 0));
     if (t >= te) return;
-    float w[K][V], b[V], win[K][V];
-    load_taps<K, V>(p, c, n, w, b);
     const T* xr = (const T*)p.x + row * p.x_row + c;
     T* yr = (T*)p.y + (long long)row * p.L * p.C + c;
-    Seq s = find(p, row, t);
-    window<T, K, V>(p, xr, s, t, c, n, win);
-    for (; t < te; t += kBatch) {
-        uint4 raw[kBatch];
+    uint4 raw[kBatch], next[kBatch];
+    auto load = [&](int t) {
 #pragma unroll
         for (int u = 0; u < kBatch; ++u)
-            raw[u] = t + u < te ? ld_raw<T>(xr + (t + u) * p.x_tok, n, p.wide) : make_uint4(0, 0, 0, 0);
+            next[u] = t + u < te ? ld_raw<T>(xr + (t + u) * p.x_tok, n, p.wide) : make_uint4(0, 0, 0, 0);
+    };
+    load(t);
+    f2 w[K][P], b[P], win[K][P];
+    load_taps<K, P>(p, c, n, w, b);
+    Seq s = find(p, row, t);
+    window<T, K, P>(p, xr, s, t, c, n, win);
+    auto one = [&](const uint4& q, int t) {
+        to_pairs(q, win[K - 1]);
+        f2 o[P];
 #pragma unroll
-        for (int u = 0; u < kBatch; ++u) {
-            if (t + u >= te) break;
-            if (p.cu && t + u >= s.end) {
-                enter(p, s, t + u);
-                window<T, K, V>(p, xr, s, t + u, c, n, win);
+        for (int i = 0; i < P; ++i) {
+            f2 a = b[i];
+#pragma unroll
+            for (int k = 0; k < K; ++k) a = fma2(w[k][i], win[k][i], a);
+            o[i] = p.silu ? silu2(a) : a;
+#pragma unroll
+            for (int k = 0; k < K - 1; ++k) win[k][i] = win[k + 1][i];
+        }
+        st_pairs<T, P>(yr + (long long)t * p.C, o, n, p.wide);
+    };
+    for (; t < te; t += kBatch) {
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) raw[u] = next[u];
+        load(t + kBatch);                                         // in flight while the present batch is worked on
+        if (t + kBatch <= te && (!p.cu || (t + kBatch <= s.end && s.q < p.S))) {
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u) one(raw[u], t + u);
+        } else {
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u) {
+                if (t + u >= te) break;
+                if (p.cu && t + u >= s.end) {
+                    enter(p, s, t + u);
+                    window<T, K, P>(p, xr, s, t + u, c, n, win);
+                }
+                if (p.cu && s.q >= p.S) return;                   // behind the last sequence
+                one(raw[u], t + u);
             }
-            if (p.cu && s.q >= p.S) return;                       // behind the last sequence
-            unpack_raw<T>(raw[u], win[K - 1]);
-            float o[V];
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                float a = b[i];
-#pragma unroll
-                for (int k = 0; k < K; ++k) a = fmaf(w[k][i], win[k][i], a);
-                o[i] = p.silu ? silu(a) : a;
-#pragma unroll
-                for (int k = 0; k < K - 1; ++k) win[k][i] = win[k + 1][i];
-            }
-            st_vec<T>(yr + (long long)(t + u) * p.C, o, n, p.wide);
         }
     }
 }
 
 // The last K - 1 inputs of every sequence. Thread = (sequence, channel); it reads all of its channel's
-// rows before it writes them, so state may be state0.
+// rows before it writes them, so that state may be state0 (then in a launch of its own, behind the
+// one that reads state0).
 template <typename T, int K>
-__global__ void k_conv_state(const ConvArgs p) {
-    const long long id = (long long)blockIdx.x * blockDim.x + threadIdx.x;
+__device__ void last_inputs(const ConvArgs& p, long long id) {
     const int c = (int)(id % p.C);
     const long long q = id / p.C;
     if (q >= p.S) return;
@@ -167,6 +216,11 @@ __global__ void k_conv_state(const ConvArgs p) {
     for (int j = 0; j < K - 1; ++j) ((T*)p.state)[(q * (K - 1) + j) * p.C + c] = v[j];
 }
 
+template <typename T, int K>
+__global__ void k_conv_state(const ConvArgs p) {
+    last_inputs<T, K>(p, (long long)blockIdx.x * blockDim.x + threadIdx.x);
+}
+
 // ------------------------------------------------------------------------------------ backward
 //   du_t = dy_t (slope of silu at u_t);  dx_t = sum_k w_k du_{t+K-1-k};  dw_k = sum_t du_t x_{t-K+1+k}
 // A thread walks a run forward, forming u_t again from the inputs, with the K sums of dx that du_t
@@ -177,18 +231,20 @@ constexpr int kVB = 4, kRows = 4;
 
 template <typename T, int K>
 __global__ void __launch_bounds__(128) k_conv_bwd(const ConvArgs p) {
+    constexpr int P = kVB / 2;
     __shared__ float red[kRows][K + 1][32 * kVB];
     const int lane = threadIdx.x & 31, grp = threadIdx.x >> 5;
     const int c = (blockIdx.x * 32 + lane) * kVB, n = p.C - c;
-    float w[K][kVB], b[kVB], dw[K][kVB], db[kVB];
+    const f2 zero = pack(0.f, 0.f);
+    f2 w[K][P], b[P], dw[K][P], db[P];
 #pragma unroll
-    for (int i = 0; i < kVB; ++i) {
-        db[i] = 0.f;
+    for (int i = 0; i < P; ++i) {
+        db[i] = zero;
 #pragma unroll
-        for (int k = 0; k < K; ++k) dw[k][i] = 0.f;
+        for (int k = 0; k < K; ++k) dw[k][i] = zero;
     }
     if (n > 0) {
-        load_taps<K, kVB>(p, c, n, w, b);
+        load_taps<K, P>(p, c, n, w, b);
         const long long all = (long long)p.B * p.runs;
         for (long long rr = (long long)blockIdx.y * kRows + grp; rr < all; rr += (long long)gridDim.y * kRows) {
             const int row = (int)(rr / p.runs);
@@ -201,36 +257,85 @@ __global__ void __launch_bounds__(128) k_conv_bwd(const ConvArgs p) {
             T* dr = (T*)p.dx + (long long)row * p.L * p.C + c;
             Seq s = find(p, row, ta);
             if (p.cu && s.q >= p.S) continue;
-            float win[K][kVB], acc[K][kVB], run_dw[K][kVB], run_db[kVB];
-            window<T, K, kVB>(p, xr, s, ta, c, n, win);
-#pragma unroll
-            for (int i = 0; i < kVB; ++i) {
-                run_db[i] = 0.f;
-#pragma unroll
-                for (int k = 0; k < K; ++k) acc[k][i] = run_dw[k][i] = 0.f;
-            }
-            // writes token `at`'s sum, held in v, if the run owns it
-            auto put = [&](int at, float (&v)[kVB]) {
-                if (at < ta || at < s.start || at >= tb) return;
-                const int m = at - s.end + K - 1;                 // its row in the state behind the sequence
-                if (m >= 0 && p.dstate) {
-                    float d[kVB];
-                    ld_ch<T, kVB>((const T*)p.dstate + ((long long)s.q * (K - 1) + m) * p.C + c, d, n, p.wide);
-#pragma unroll
-                    for (int i = 0; i < kVB; ++i) v[i] += d[i];
-                }
-                st_ch<T, kVB>(dr + (long long)at * p.C, v, n, p.wide);
-            };
             const int stop = min(tb + K - 1, p.L);
-            int t = ta;
-            bool open = true;
-            for (; open && t < stop; t += kBatch) {
-                float xs[kBatch][kVB], gs[kBatch][kVB];
+            typename Raw<T, P>::type xs[kBatch], gs[kBatch], xn[kBatch], gn[kBatch];
+            auto load = [&](int t) {
 #pragma unroll
                 for (int u = 0; u < kBatch; ++u) {
                     const bool in = t + u < stop;
-                    ld_ch<T, kVB>(xr + (in ? (t + u) * p.x_tok : 0), xs[u], in ? n : 0, p.wide);
-                    ld_ch<T, kVB>(gr + (in ? (long long)(t + u) * p.C : 0), gs[u], in ? n : 0, p.wide);
+                    xn[u] = ld_pairs_raw<T, P>(xr + (in ? (t + u) * p.x_tok : 0), in ? n : 0, p.wide);
+                    gn[u] = ld_pairs_raw<T, P>(gr + (in ? (long long)(t + u) * p.C : 0), in ? n : 0, p.wide);
+                }
+            };
+            load(ta);
+            f2 win[K][P], acc[K][P], run_dw[K][P], run_db[P];
+            window<T, K, P>(p, xr, s, ta, c, n, win);
+#pragma unroll
+            for (int i = 0; i < P; ++i) {
+                run_db[i] = zero;
+#pragma unroll
+                for (int k = 0; k < K; ++k) acc[k][i] = run_dw[k][i] = zero;
+            }
+            // writes token `at`'s sum, held in v, if the run owns it
+            auto put = [&](int at, f2 (&v)[P]) {
+                if (at < ta || at < s.start || at >= tb) return;
+                const int m = at - s.end + K - 1;                 // its row in the state behind the sequence
+                if (m >= 0 && p.dstate) {
+                    f2 d[P];
+                    to_pairs(ld_pairs_raw<T, P>((const T*)p.dstate + ((long long)s.q * (K - 1) + m) * p.C + c, n, p.wide), d);
+#pragma unroll
+                    for (int i = 0; i < P; ++i) v[i] = add2(v[i], d[i]);
+                }
+                st_pairs<T, P>(dr + (long long)at * p.C, v, n, p.wide);
+            };
+            // token t: its du into the sums of dx, and of dw if the run owns it
+            auto one = [&](int u, bool own) {
+                to_pairs(xs[u], win[K - 1]);
+                f2 g[P];
+                to_pairs(gs[u], g);
+#pragma unroll
+                for (int i = 0; i < P; ++i) {
+                    f2 du = g[i];
+                    if (p.silu) {
+                        f2 a = b[i];
+#pragma unroll
+                        for (int k = 0; k < K; ++k) a = fma2(w[k][i], win[k][i], a);
+                        du = mul2(du, silu_slope2(a));
+                    }
+#pragma unroll
+                    for (int k = 0; k < K; ++k) acc[k][i] = fma2(w[k][i], du, acc[k][i]);
+                    if (own) {
+                        run_db[i] = add2(run_db[i], du);
+#pragma unroll
+                        for (int k = 0; k < K; ++k) run_dw[k][i] = fma2(du, win[k][i], run_dw[k][i]);
+                    }
+                }
+            };
+            auto shift = [&] {
+#pragma unroll
+                for (int i = 0; i < P; ++i) {
+#pragma unroll
+                    for (int k = 0; k < K - 1; ++k) {
+                        acc[k][i] = acc[k + 1][i];
+                        win[k][i] = win[k + 1][i];
+                    }
+                    acc[K - 1][i] = zero;
+                }
+            };
+            bool open = true;
+            for (int t = ta; open && t < stop; t += kBatch) {
+#pragma unroll
+                for (int u = 0; u < kBatch; ++u) { xs[u] = xn[u]; gs[u] = gn[u]; }
+                load(t + kBatch);
+                if (t >= max(ta, s.start) + K - 1 && t + kBatch <= min(tb, s.end)) {
+                    // all within the run and one sequence: every token completes one that the run owns
+#pragma unroll
+                    for (int u = 0; u < kBatch; ++u) {
+                        one(u, true);
+                        st_pairs<T, P>(dr + (long long)(t + u - (K - 1)) * p.C, acc[0], n, p.wide);
+                        shift();
+                    }
+                    continue;
                 }
 #pragma unroll
                 for (int u = 0; u < kBatch; ++u) {
@@ -245,40 +350,15 @@ __global__ void __launch_bounds__(128) k_conv_bwd(const ConvArgs p) {
                             open = s.q < p.S;
                         }
                         if (!open) break;
-                        window<T, K, kVB>(p, xr, s, tt, c, n, win);
+                        window<T, K, P>(p, xr, s, tt, c, n, win);
 #pragma unroll
                         for (int k = 0; k < K; ++k)
 #pragma unroll
-                            for (int i = 0; i < kVB; ++i) acc[k][i] = 0.f;
+                            for (int i = 0; i < P; ++i) acc[k][i] = zero;
                     }
-#pragma unroll
-                    for (int i = 0; i < kVB; ++i) {
-                        win[K - 1][i] = xs[u][i];
-                        float du = gs[u][i];
-                        if (p.silu) {
-                            float a = b[i];
-#pragma unroll
-                            for (int k = 0; k < K; ++k) a = fmaf(w[k][i], win[k][i], a);
-                            du *= silu_slope(a);
-                        }
-#pragma unroll
-                        for (int k = 0; k < K; ++k) acc[k][i] = fmaf(w[k][i], du, acc[k][i]);
-                        if (tt < tb) {
-                            run_db[i] += du;
-#pragma unroll
-                            for (int k = 0; k < K; ++k) run_dw[k][i] = fmaf(du, win[k][i], run_dw[k][i]);
-                        }
-                    }
+                    one(u, tt < tb);
                     put(tt - (K - 1), acc[0]);
-#pragma unroll
-                    for (int i = 0; i < kVB; ++i) {
-#pragma unroll
-                        for (int k = 0; k < K - 1; ++k) {
-                            acc[k][i] = acc[k + 1][i];
-                            win[k][i] = win[k + 1][i];
-                        }
-                        acc[K - 1][i] = 0.f;
-                    }
+                    shift();
                 }
             }
             if (open && stop == s.end) {                          // ended with the sequence, inside the loop's last batch
@@ -286,18 +366,20 @@ __global__ void __launch_bounds__(128) k_conv_bwd(const ConvArgs p) {
                 for (int k = 0; k < K - 1; ++k) put(stop - (K - 1) + k, acc[k]);
             }
 #pragma unroll
-            for (int i = 0; i < kVB; ++i) {
-                db[i] += run_db[i];
+            for (int i = 0; i < P; ++i) {
+                db[i] = add2(db[i], run_db[i]);
 #pragma unroll
-                for (int k = 0; k < K; ++k) dw[k][i] += run_dw[k][i];
+                for (int k = 0; k < K; ++k) dw[k][i] = add2(dw[k][i], run_dw[k][i]);
             }
         }
     }
 #pragma unroll
-    for (int i = 0; i < kVB; ++i) {
+    for (int i = 0; i < P; ++i) {
 #pragma unroll
-        for (int k = 0; k < K; ++k) red[grp][k][lane * kVB + i] = dw[k][i];
-        red[grp][K][lane * kVB + i] = db[i];
+        for (int k = 0; k <= K; ++k) {
+            const float2 v = unpack(k < K ? dw[k][i] : db[i]);
+            *(float2*)&red[grp][k][lane * kVB + 2 * i] = v;
+        }
     }
     __syncthreads();
     for (int e = threadIdx.x; e < (K + 1) * 32 * kVB; e += blockDim.x) {
@@ -310,13 +392,23 @@ __global__ void __launch_bounds__(128) k_conv_bwd(const ConvArgs p) {
     }
 }
 
-// dw and dbias: the blocks' sums in order. Thread = (tap or bias, channel).
+// dw and dbias: the blocks' sums, 32 (tap or bias, channel) pairs a block, each by eight threads that take
+// every eighth block; their sums are added in order.
 __global__ void k_conv_sum(const float* part, int blocks, int C, int K, float* dw, float* dbias) {
-    const int i = blockIdx.x * blockDim.x + threadIdx.x;
-    if (i >= (K + 1) * C) return;
-    const int k = i / C, c = i % C;
+    __shared__ float red[8][32];
+    const int i = blockIdx.x * 32 + threadIdx.x, n = (K + 1) * C;
     float v = 0.f;
-    for (int g = 0; g < blocks; ++g) v += part[((long long)g * (K + 1) + k) * C + c];
+    if (i < n) {
+#pragma unroll 4
+        for (int g = threadIdx.y; g < blocks; g += 8) v += part[(long long)g * n + i];
+    }
+    red[threadIdx.y][threadIdx.x] = v;
+    __syncthreads();
+    if (threadIdx.y != 0 || i >= n) return;
+    v = 0.f;
+#pragma unroll
+    for (int g = 0; g < 8; ++g) v += red[g][threadIdx.x];
+    const int k = i / C, c = i % C;
     if (k < K) dw[(long long)c * K + k] = v;
     else if (dbias) dbias[c] = v;
 }
@@ -381,30 +473,50 @@ __global__ void __launch_bounds__(128) k_conv_step(const ConvArgs p, const int* 
         if (__syncthreads_or(earlier)) return;
         more = __syncthreads_or(later);
     }
+    constexpr int P = V / 2;
     const int c = (blockIdx.x * blockDim.x + threadIdx.x) * V, n = p.C - c;
     if (n <= 0) return;
     T* st = (T*)p.state + (long long)slot * (K - 1) * p.C + c;
-    float win[K][V], w[K][V], bias[V];
+    uint4 win[K];
+    f2 w[K][P], bias[P];
 #pragma unroll
-    for (int j = 0; j < K - 1; ++j) ld_ch<T, V>(st + (long long)j * p.C, win[j], n, p.wide);
-    load_taps<K, V>(p, c, n, w, bias);
+    for (int j = 0; j < K - 1; ++j) win[j] = ld_raw<T>(st + (long long)j * p.C, n, p.wide);
+    win[K - 1] = ld_raw<T>((const T*)p.x + b0 * p.x_row + c, n, p.wide);
+    load_taps<K, P>(p, c, n, w, bias);
     for (int b = b0; b < (more ? p.B : b0 + 1); ++b) {
-        if (b != b0 && idx[b] != slot) continue;
-        ld_ch<T, V>((const T*)p.x + b * p.x_row + c, win[K - 1], n, p.wide);
-        float o[V];
+        if (b != b0) {
+            if (idx[b] != slot) continue;
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            float a = bias[i];
-#pragma unroll
-            for (int k = 0; k < K; ++k) a = fmaf(w[k][i], win[k][i], a);
-            o[i] = p.silu ? silu(a) : a;
-#pragma unroll
-            for (int k = 0; k < K - 1; ++k) win[k][i] = win[k + 1][i];
+            for (int k = 0; k < K - 1; ++k) win[k] = win[k + 1];
+            win[K - 1] = ld_raw<T>((const T*)p.x + b * p.x_row + c, n, p.wide);
         }
-        st_ch<T, V>((T*)p.y + (long long)b * p.C + c, o, n, p.wide);
+        f2 o[P];
+#pragma unroll
+        for (int i = 0; i < P; ++i) o[i] = bias[i];
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            f2 v[P];
+            to_pairs(win[k], v);
+#pragma unroll
+            for (int i = 0; i < P; ++i) o[i] = fma2(w[k][i], v[i], o[i]);
+        }
+        if (p.silu) {
+#pragma unroll
+            for (int i = 0; i < P; ++i) o[i] = silu2(o[i]);
+        }
+        st_pairs<T, P>((T*)p.y + (long long)b * p.C + c, o, n, p.wide);
     }
 #pragma unroll
-    for (int j = 0; j < K - 1; ++j) st_ch<T, V>(st + (long long)j * p.C, win[j], n, p.wide);
+    for (int j = 0; j < K - 1; ++j) {
+        T* to = st + (long long)j * p.C;
+        if (p.wide && n >= V) {
+            *(uint4*)to = win[j + 1];
+        } else {
+            float f[V];
+            unpack_raw<T>(win[j + 1], f);
+            st_vec<T>(to, f, n, false);
+        }
+    }
 }
 
 // ---------------------------------------------------------------------------------------- host
@@ -476,6 +588,7 @@ gspn_status gspn_conv_forward(const gspn_conv_desc* desc, const void* x, const f
         if (!aligned_to(q, 4)) return GSPN_ERR_ALIGNMENT;
     p.x = x; p.w = w; p.bias = bias; p.cu = cu; p.state0 = state0; p.y = y; p.state = state;
     p.wide = (p.C * es) % 16 == 0 && wide_ok(x, p.x_row, p.x_tok, es) && aligned_to(y, 16) && aligned_to(state0, 16);
+    p.wide_w = aligned_to(w, 16);
     const int V = desc->dtype == GSPN_F32 ? 4 : 8;
     p.nvec = (p.C + V - 1) / V;
     // Short inputs are cut into runs of kBatch tokens, so that more threads share them.
@@ -487,11 +600,11 @@ gspn_status gspn_conv_forward(const gspn_conv_desc* desc, const void* x, const f
     with_taps(desc->dtype, desc->K, [&](auto t, auto k) {
         using T = decltype(t);
         constexpr int K = decltype(k)::value;
-        if (total > 0) k_conv_fwd<T, K><<<(unsigned)((total + 127) / 128), 128, 0, st>>>(p);
-        if (state) {
-            const long long n = (long long)p.S * p.C;
-            k_conv_state<T, K><<<(unsigned)((n + 127) / 128), 128, 0, st>>>(p);
-        }
+        const long long blocks = (total + 127) / 128, behind = state ? ((long long)p.S * p.C + 127) / 128 : 0;
+        const bool apart = state == state0;                       // no thread of this launch may still read state0
+        if (blocks + (apart ? 0 : behind) > 0)
+            k_conv_fwd<T, K><<<(unsigned)(blocks + (apart ? 0 : behind)), 128, 0, st>>>(p, blocks);
+        if (apart && behind > 0) k_conv_state<T, K><<<(unsigned)behind, 128, 0, st>>>(p);
     });
     return last_status();
 }
@@ -517,6 +630,7 @@ gspn_status gspn_conv_backward(const gspn_conv_desc* desc, const void* x, const 
     p.part = (float*)((char*)ws + 256);
     p.wide = (p.C * es) % 16 == 0 && wide_ok(x, p.x_row, p.x_tok, es) && aligned_to(dy, 16) && aligned_to(dx, 16) &&
              aligned_to(state0, 16) && aligned_to(dstate, 16);
+    p.wide_w = aligned_to(w, 16);
     p.run = kRunBwd;
     p.runs = (p.L + kRunBwd - 1) / kRunBwd;
     const int gy = bwd_blocks(*desc);
@@ -526,7 +640,7 @@ gspn_status gspn_conv_backward(const gspn_conv_desc* desc, const void* x, const 
         constexpr int K = decltype(k)::value;
         const dim3 grid((p.C + 32 * kVB - 1) / (32 * kVB), gy);
         k_conv_bwd<T, K><<<grid, 128, 0, st>>>(p);
-        k_conv_sum<<<((K + 1) * p.C + 127) / 128, 128, 0, st>>>(p.part, gy, p.C, K, dw, dbias);
+        k_conv_sum<<<((K + 1) * p.C + 31) / 32, dim3(32, 8), 0, st>>>(p.part, gy, p.C, K, dw, dbias);
         if (dstate0) {
             const long long n = (long long)p.S * p.C;
             k_conv_dstate<T, K><<<(unsigned)((n + 127) / 128), 128, 0, st>>>(p);
@@ -548,6 +662,7 @@ gspn_status gspn_conv_step(const gspn_conv_desc* desc, const void* x, const floa
         if (!aligned_to(q, 4)) return GSPN_ERR_ALIGNMENT;
     p.x = x; p.w = w; p.bias = bias; p.y = y; p.state = state;
     p.wide = (p.C * es) % 16 == 0 && wide_ok(x, p.x_row, 0, es) && aligned_to(y, 16) && aligned_to(state, 16);
+    p.wide_w = aligned_to(w, 16);
     const int V = desc->dtype == GSPN_F32 ? 4 : 8;
     const int nvec = (p.C + V - 1) / V;
     cudaStream_t st = (cudaStream_t)stream;

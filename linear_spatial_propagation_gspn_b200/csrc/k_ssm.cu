@@ -7,7 +7,7 @@
 // exponential for each (t, c, n), which the special-function unit makes at 16 a cycle and SM.
 //
 // Layout of a block: 32 channels of one sequence (64 bytes of a bf16 row: whole sectors) and
-// NL = ceil(N / 4) rounded up to 2, 4, 8 or 16 lanes for each channel, four states in registers per
+// NL = ceil(N / 4) rounded up to 4, 8 or 16 lanes for each channel, four states in registers per
 // lane. Tokens come in tiles of 32: each thread loads its part of the next tile into registers
 // while the present one is scanned from shared memory, where the steps d and d x are formed once
 // per (t, c). Sums over n stay in the NL lanes of a channel: four tokens at a time are reduced and
@@ -171,20 +171,15 @@ template <int NL> struct YRow {
     // the sum of channel c's shares; row is 16-byte aligned
     static __device__ __forceinline__ float sum(const float* row, int c) {
         const float* s = row + at(c, 0);
-        if constexpr (NL == 2) {
-            const float2 v = *(const float2*)s;
-            return v.x + v.y;
-        } else {
-            float w = 0.f;
+        float w = 0.f;
 #pragma unroll
-            for (int k = 0; k < NL; k += 4) {
-                f2 a, b;
-                ld_pairs(s + k, a, b);
-                const float2 v = unpack(add2(a, b));
-                w += v.x + v.y;
-            }
-            return w;
+        for (int k = 0; k < NL; k += 4) {
+            f2 a, b;
+            ld_pairs(s + k, a, b);
+            const float2 v = unpack(add2(a, b));
+            w += v.x + v.y;
         }
+        return w;
     }
 };
 
@@ -545,31 +540,40 @@ constexpr int kScanRegs = 248, kFeedRegs = 128;                   // 168 each at
 template <int NL> struct Bwd {
     static constexpr int CH = 256 / NL;                           // channels of a block
     static constexpr int QR = CH / kQ;                            // vectors of four channels in a token
-    static constexpr int quads = kTB * QR, NV = (quads + kFeedB - 1) / kFeedB, active = quads < kFeedB ? quads : kFeedB;
+    static constexpr int quads = kTB * QR, active = quads;        // one for each feeding thread, at most
     static constexpr int states = kTB * 4 * NL, NS = (states + kFeedB - 1) / kFeedB;
     static constexpr int PC = perm_copies(NL), W = NL / 2;        // orders of B and C; shares of a sum over n
 };
 // Rows of pairs (d, d x), and of the shares of a sum over n: padded as in the forward pass.
 template <int NL> struct PRow {
-    static constexpr int vec = kQ + 2, len = Bwd<NL>::QR * vec;   // in pairs
+    static constexpr int vec = kQ + 1, len = Bwd<NL>::QR * vec;   // in entries of 16 bytes
     static __device__ __forceinline__ int at(int c) { return c / kQ * vec + c % kQ; }
 };
 template <int NL> struct ORow {
     static constexpr int W = Bwd<NL>::W, vec = kQ * W + 4, len = Bwd<NL>::QR * vec;
     static __device__ __forceinline__ int at(int c, int w) { return c / kQ * vec + c % kQ * W + w; }
-    static __device__ __forceinline__ float sum(const float* row, int c) {
+    // the sums of the four channels from c on (a multiple of four)
+    static __device__ __forceinline__ void sum(const float* row, int c, float (&o)[kQ]) {
         const float* s = row + at(c, 0);
-        float v = s[0];
+        float f[kQ * W];
 #pragma unroll
-        for (int k = 1; k < W; ++k) v += s[k];
-        return v;
+        for (int k = 0; k < kQ * W; k += 4) {
+            const float4 v = *(const float4*)(s + k);
+            f[k] = v.x; f[k + 1] = v.y; f[k + 2] = v.z; f[k + 3] = v.w;
+        }
+#pragma unroll
+        for (int j = 0; j < kQ; ++j) {
+            o[j] = f[j * W];
+#pragma unroll
+            for (int k = 1; k < W; ++k) o[j] += f[j * W + k];
+        }
     }
 };
 
 template <typename T, int NL> struct BwdSmem {
-    float2 dd[2][kTB][PRow<NL>::len];
-    float r[2][kTB][Bwd<NL>::CH];                                 // dy silu(z)
-    BC4<T> bc[2][kTB][Bwd<NL>::PC][NL];
+    float4 dd[2][kTB][PRow<NL>::len];                             // d, d, d x, d x
+    float2 r[2][kTB][Bwd<NL>::CH];                                // dy silu(z), twice
+    float4 B[2][kTB][Bwd<NL>::PC][NL], C[2][kTB][Bwd<NL>::PC][NL];   // in fp32: unpacking costs the scan more than the loads
     float o[2][3][kTB][ORow<NL>::len];                            // C h, g B, e A: shares of the sums over n
     float sum[2][kScan / 32][kTB][8 * NL];                        // dB, dC: sums over a warp's channels
 };
@@ -599,24 +603,19 @@ __global__ void __launch_bounds__(kScan + kFeedB, 1) k_ssm_bwd(const SsmArgs p) 
             sD[j] = sb[j] = 0.f;
         }
         // x, dt, z, dy: of the tile in flight, of the one staged last and of the one staged before it
-        Raw rr[4][W::NV], k1[4][W::NV], k0[4][W::NV];
+        Raw rr[4], k1[4], k0[4];
         T rB[W::NS], rC[W::NS];
         auto load = [&](int i) {
             if (i < 0) return;
-            const int t0 = q.lo + i * kTB;
-            auto one = [&](Raw (&r)[W::NV], const void* base, long long row, long long tok) {
-#pragma unroll
-                for (int k = 0; k < W::NV; ++k) {
-                    const int v = k * kFeedB + tid, t = t0 + v / W::QR;
-                    r[k] = Raw{};
-                    if (v < W::quads && t < q.hi)
-                        r[k] = ld_quad((const T*)base + q.sp.row * row + (q.sp.first + t) * tok + q.c0 + vc, q.nc - vc, p.wide);
-                }
+            const int t0 = q.lo + i * kTB, t = t0 + tid / W::QR;
+            const bool in = tid < W::quads && t < q.hi;
+            auto one = [&](const void* base, long long row, long long tok) {
+                return in ? ld_quad((const T*)base + q.sp.row * row + (q.sp.first + t) * tok + q.c0 + vc, q.nc - vc, p.wide) : Raw{};
             };
-            one(rr[0], p.x, p.x_row, p.x_tok);
-            one(rr[1], p.dt, p.dt_row, p.dt_tok);
-            if (p.z) one(rr[2], p.z, p.z_row, p.z_tok);
-            one(rr[3], p.dy, (long long)p.L * p.C, p.C);
+            rr[0] = one(p.x, p.x_row, p.x_tok);
+            rr[1] = one(p.dt, p.dt_row, p.dt_tok);
+            rr[2] = p.z ? one(p.z, p.z_row, p.z_tok) : Raw{};
+            rr[3] = one(p.dy, (long long)p.L * p.C, p.C);
 #pragma unroll
             for (int k = 0; k < W::NS; ++k) {
                 const int e = k * kFeedB + tid, t = t0 + e / (4 * NL), n = e % (4 * NL);
@@ -629,17 +628,16 @@ __global__ void __launch_bounds__(kScan + kFeedB, 1) k_ssm_bwd(const SsmArgs p) 
         };
         auto stage = [&](int i) {
             const int t0 = q.lo + i * kTB, buf = i & 1;
+            {
+                const int t = tid / W::QR;
 #pragma unroll
-            for (int k = 0; k < W::NV; ++k) {
-                const int v = k * kFeedB + tid, t = v / W::QR;
-#pragma unroll
-                for (int m = 0; m < 4; ++m) { k0[m][k] = k1[m][k]; k1[m][k] = rr[m][k]; }
-                if (W::active == kFeedB || v < W::quads) {
+                for (int m = 0; m < 4; ++m) { k0[m] = k1[m]; k1[m] = rr[m]; }
+                if (W::active == kFeedB || tid < W::quads) {
                     float xv[kQ], dv[kQ], zv[kQ], gv[kQ];
-                    unpack_quad(rr[0][k], xv);
-                    unpack_quad(rr[1][k], dv);
-                    unpack_quad(rr[2][k], zv);
-                    unpack_quad(rr[3][k], gv);
+                    unpack_quad(rr[0], xv);
+                    unpack_quad(rr[1], dv);
+                    unpack_quad(rr[2], zv);
+                    unpack_quad(rr[3], gv);
                     const bool ok = t0 + t < q.hi;                // behind the end: no step; x and dy were read as zero
                     float r[kQ];
 #pragma unroll
@@ -648,11 +646,13 @@ __global__ void __launch_bounds__(kScan + kFeedB, 1) k_ssm_bwd(const SsmArgs p) 
                         if (p.softplus) d = softplus_of(d);
                         if (!ok) d = make_float2(0.f, 0.f);
                         const float2 w = unpack(mul2(pack(d.x, d.y), pack(xv[j], xv[j + 1])));
-                        *(float4*)&sm.dd[buf][t][PRow<NL>::at(vc + j)] = make_float4(d.x, w.x, d.y, w.y);
+                        sm.dd[buf][t][PRow<NL>::at(vc + j)] = make_float4(d.x, d.x, w.x, w.x);
+                        sm.dd[buf][t][PRow<NL>::at(vc + j + 1)] = make_float4(d.y, d.y, w.y, w.y);
                         r[j] = p.z ? gv[j] * silu(zv[j]) : gv[j];
                         r[j + 1] = p.z ? gv[j + 1] * silu(zv[j + 1]) : gv[j + 1];
                     }
-                    *(float4*)&sm.r[buf][t][vc] = make_float4(r[0], r[1], r[2], r[3]);
+                    *(float4*)&sm.r[buf][t][vc] = make_float4(r[0], r[0], r[1], r[1]);
+                    *(float4*)&sm.r[buf][t][vc + 2] = make_float4(r[2], r[2], r[3], r[3]);
                 }
             }
 #pragma unroll
@@ -661,9 +661,8 @@ __global__ void __launch_bounds__(kScan + kFeedB, 1) k_ssm_bwd(const SsmArgs p) 
                 if (W::states >= kFeedB || e < W::states) {
 #pragma unroll
                     for (int m = 0; m < PC; ++m) {
-                        T* to = sm.bc[buf][t][m][n / 4].v + (n % 4 ^ m);
-                        to[0] = rB[k];
-                        to[4] = rC[k];
+                        ((float*)&sm.B[buf][t][m][n / 4])[n % 4 ^ m] = Io<T>::ld(&rB[k]);
+                        ((float*)&sm.C[buf][t][m][n / 4])[n % 4 ^ m] = Io<T>::ld(&rC[k]);
                     }
                 }
             }
@@ -671,23 +670,24 @@ __global__ void __launch_bounds__(kScan + kFeedB, 1) k_ssm_bwd(const SsmArgs p) 
         // Gradients of tile i (the one staged before the last) from the complete sums.
         auto finish = [&](int i) {
             const int t0 = q.lo + i * kTB, buf = i & 1;
-#pragma unroll
-            for (int k = 0; k < W::NV; ++k) {
-                const int v = k * kFeedB + tid, t = v / W::QR;
-                if (v < W::quads && t0 + t < q.hi) {
-                    float xv[kQ], dv[kQ], zv[kQ], gv[kQ], ox[kQ], od[kQ], oz[kQ];
-                    unpack_quad(k0[0][k], xv);
-                    unpack_quad(k0[1][k], dv);
-                    unpack_quad(k0[2][k], zv);
-                    unpack_quad(k0[3][k], gv);
+            {
+                const int t = tid / W::QR;
+                if (tid < W::quads && t0 + t < q.hi) {
+                    float xv[kQ], dv[kQ], zv[kQ], gv[kQ], ox[kQ], od[kQ], oz[kQ], ys[kQ], gBs[kQ], eAs[kQ];
+                    unpack_quad(k0[0], xv);
+                    unpack_quad(k0[1], dv);
+                    unpack_quad(k0[2], zv);
+                    unpack_quad(k0[3], gv);
+                    ORow<NL>::sum(sm.o[buf][0][t], vc, ys);
+                    ORow<NL>::sum(sm.o[buf][1][t], vc, gBs);
+                    ORow<NL>::sum(sm.o[buf][2][t], vc, eAs);
 #pragma unroll
                     for (int j = 0; j < kQ; ++j) {
-                        const float gB = ORow<NL>::sum(sm.o[buf][1][t], vc + j);
-                        const float eA = ORow<NL>::sum(sm.o[buf][2][t], vc + j) * kLn2;
+                        const float gB = gBs[j], eA = eAs[j] * kLn2;
                         const float d = sm.dd[buf][t][PRow<NL>::at(vc + j)].x;
                         float r = gv[j];
                         if (p.z) {
-                            const float y = fmaf(Dv[j], xv[j], ORow<NL>::sum(sm.o[buf][0][t], vc + j));
+                            const float y = fmaf(Dv[j], xv[j], ys[j]);
                             const float s = sigmoid(zv[j]);
                             oz[j] = gv[j] * y * fmaf(zv[j] * s, 1.f - s, s);
                             r *= zv[j] * s;
@@ -729,9 +729,7 @@ __global__ void __launch_bounds__(kScan + kFeedB, 1) k_ssm_bwd(const SsmArgs p) 
                 load(i - 2);
             } else {
 #pragma unroll
-                for (int k = 0; k < W::NV; ++k)
-#pragma unroll
-                    for (int m = 0; m < 4; ++m) k0[m][k] = k1[m][k];
+                for (int m = 0; m < 4; ++m) k0[m] = k1[m];
             }
             __syncthreads();
             finish(i);                                            // d of tile i is overwritten behind the next barrier only
@@ -822,13 +820,12 @@ __global__ void __launch_bounds__(kScan + kFeedB, 1) k_ssm_bwd(const SsmArgs p) 
         load_h(i - 1);
 #pragma unroll
         for (int t = 0; t < kTB; ++t) {
-            float bb[4];
-            get_b(sm.bc[buf][t][pm][nl], bb);
-            const f2 b01 = pack(bb[0], bb[1]), b23 = pack(bb[2], bb[3]);
+            f2 b01, b23;
+            ld_pairs((const float*)&sm.B[buf][t][pm][nl], b01, b23);
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
-                const float2 dd = sm.dd[buf][t][PRow<NL>::at(cl[s])];
-                const f2 d = both(dd.x), dx = both(dd.y);
+                f2 d, dx;
+                ld_pairs((const float*)&sm.dd[buf][t][PRow<NL>::at(cl[s])], d, dx);
                 h[t][s][0] = fma2(ex2_2(mul2(d, A2[s][0])), t ? h[t - 1][s][0] : hin[s][0], mul2(dx, b01));
                 h[t][s][1] = fma2(ex2_2(mul2(d, A2[s][1])), t ? h[t - 1][s][1] : hin[s][1], mul2(dx, b23));
             }
@@ -836,17 +833,29 @@ __global__ void __launch_bounds__(kScan + kFeedB, 1) k_ssm_bwd(const SsmArgs p) 
         f2 dAs[2][2];                                             // sums of 16 tokens join the long sum as one
 #pragma unroll
         for (int s = 0; s < 2; ++s) dAs[s][0] = dAs[s][1] = pack(0.f, 0.f);
+        // A token's operands are fetched before the stores of the one ahead of it, which would hold them back.
+        f2 od[2][2], odx[2][2], orr[2][2], ob[2][2], oc2[2][2];
+        auto fetch = [&](int t) {
+            const int w = t & 1;
+            ld_pairs((const float*)&sm.B[buf][t][pm][nl], ob[w][0], ob[w][1]);
+            ld_pairs((const float*)&sm.C[buf][t][pm][nl], oc2[w][0], oc2[w][1]);
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                ld_pairs((const float*)&sm.dd[buf][t][PRow<NL>::at(cl[s])], od[w][s], odx[w][s]);
+                orr[w][s] = *(const f2*)&sm.r[buf][t][cl[s]];
+            }
+        };
+        fetch(kTB - 1);
 #pragma unroll
         for (int t = kTB - 1; t >= 0; --t) {
-            float bb[4], cc[4];
-            get_bc(sm.bc[buf][t][pm][nl], bb, cc);
-            const f2 b2[2] = {pack(bb[0], bb[1]), pack(bb[2], bb[3])}, c2[2] = {pack(cc[0], cc[1]), pack(cc[2], cc[3])};
+            if (t > 0) fetch(t - 1);
+            const f2 (&b2)[2] = ob[t & 1];
+            const f2 (&c2)[2] = oc2[t & 1];
             f2 vB[2], vC[2];
             float yv[2], gv[2], ev[2];
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
-                const float2 dd = sm.dd[buf][t][PRow<NL>::at(cl[s])];
-                const f2 d = both(dd.x), dx = both(dd.y), r = both(sm.r[buf][t][cl[s]]);
+                const f2 d = od[t & 1][s], dx = odx[t & 1][s], r = orr[t & 1][s];
                 f2 y, gb, ea;
 #pragma unroll
                 for (int m = 0; m < 2; ++m) {
@@ -889,9 +898,7 @@ __global__ void __launch_bounds__(kScan + kFeedB, 1) k_ssm_bwd(const SsmArgs p) 
                     out[4 * NL + n0 + pm] = vc;
                 } else {
                     const bool up = ql & 4;
-                    float w = (up ? vc : vb) + __shfl_xor_sync(all, up ? vb : vc, 4 * NL);
-                    if constexpr (NL == 2) w += __shfl_xor_sync(all, w, 8 * NL);
-                    if (NL != 2 || ql < 8) out[(up ? 4 * NL : 0) + n0 + pm] = w;
+                    out[(up ? 4 * NL : 0) + n0 + pm] = (up ? vc : vb) + __shfl_xor_sync(all, up ? vb : vc, 4 * NL);
                 }
             }
         }
@@ -1044,7 +1051,8 @@ __global__ void k_ssm_step(const SsmArgs p, const int* idx, int slots, int NL) {
 // ---------------------------------------------------------------------------------------- host
 constexpr size_t kHalfSmem = 116 * 1024;
 
-int lanes_for(int N) { return N <= 8 ? 2 : N <= 16 ? 4 : N <= 32 ? 8 : 16; }
+// Two lanes for N <= 8 were no faster than four of which half idle (4 x 2048 x 4096: 324 us forward both).
+int lanes_for(int N) { return N <= 16 ? 4 : N <= 32 ? 8 : 16; }
 
 bool make_args(const gspn_ssm_desc* d, SsmArgs* p) {
     if (!d) return false;
@@ -1127,8 +1135,7 @@ template <typename F>
 void with_lanes(int dtype, int NL, F&& f) {
     auto by = [&](auto t) {
         using T = decltype(t);
-        if (NL == 2) f(t, std::integral_constant<int, 2>());
-        else if (NL == 4) f(t, std::integral_constant<int, 4>());
+        if (NL == 4) f(t, std::integral_constant<int, 4>());
         else if (NL == 8) f(t, std::integral_constant<int, 8>());
         else f(t, std::integral_constant<int, 16>());
         (void)sizeof(T);

@@ -156,11 +156,47 @@ __device__ __forceinline__ float max_nan(float a, float b) {
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
     return r;
 }
+__device__ __forceinline__ f2 sigmoid2(f2 v) {
+    const float2 e = unpack(add2(ex2_2(mul2(v, both(-kLog2e))), both(1.f)));
+    return pack(rcp(e.x), rcp(e.y));
+}
+__device__ __forceinline__ f2 silu2(f2 v) { return mul2(v, sigmoid2(v)); }
+__device__ __forceinline__ f2 silu_slope2(f2 v) {
+    const f2 s = sigmoid2(v);
+    return fma2(mul2(v, s), fma2(s, both(-1.f), both(1.f)), s);
+}
 // Four floats of shared memory (16-byte aligned) as two pairs.
 __device__ __forceinline__ void ld_pairs(const float* p, f2& a, f2& b) {
     const ulonglong2 q = *(const ulonglong2*)p;
     a = q.x;
     b = q.y;
+}
+
+// V elements as stored (16 bytes), or four of them, as pairs.
+template <int P>
+__device__ __forceinline__ void to_pairs(const uint4& q, f2 (&v)[P]) {
+    static_assert(P == 2 || P == 4, "four fp32 or eight bf16");
+    if constexpr (P == 2) {
+        v[0] = pack(__uint_as_float(q.x), __uint_as_float(q.y));
+        v[1] = pack(__uint_as_float(q.z), __uint_as_float(q.w));
+    } else {
+        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[k] = pack(__uint_as_float(w[k] << 16), __uint_as_float(w[k] & 0xffff0000u));
+    }
+}
+__device__ __forceinline__ void to_pairs(const uint2& q, f2 (&v)[2]) {
+    v[0] = pack(__uint_as_float(q.x << 16), __uint_as_float(q.x & 0xffff0000u));
+    v[1] = pack(__uint_as_float(q.y << 16), __uint_as_float(q.y & 0xffff0000u));
+}
+template <int P>
+__device__ __forceinline__ void to_floats(const f2 (&v)[P], float (&o)[2 * P]) {
+#pragma unroll
+    for (int k = 0; k < P; ++k) {
+        const float2 f = unpack(v[k]);
+        o[2 * k] = f.x;
+        o[2 * k + 1] = f.y;
+    }
 }
 
 // ------------------------------------------------------------------ sequences
