@@ -2,9 +2,8 @@
 //   m = y silu(gate);  v = norm(m) w_post + b_post;  r_out = r + scale v;  o = norm(r_out) w_pre + b_pre
 // with norm(v) = v / sqrt(mean(v^2) + eps), of v - mean(v) when centred.
 //
-// Some tens of operations per element: memory traffic bounds it. A row stays in the registers of TPR
-// threads (one warp for narrow rows, a block for wide ones) from its load to its last store, so every
-// tensor crosses HBM once. Means are taken before squares of differences, from registers, so that
+// Some tens of operations per element: memory traffic bounds it. A row stays in the registers of one
+// warp (narrow rows) or one block from its load to its last store, so every tensor crosses HBM once. Means are taken before squares of differences, from registers, so that
 // no cancellation enters. Statistics and sums are fp32.
 #include "seq_common.cuh"
 
@@ -18,7 +17,7 @@ enum { kDwPost, kDbPost, kDscale, kDwPre, kDbPre, kSums };
 struct NormArgs {
     int rows, C, center;
     float eps, inv_c;
-    long long y_row, gate_row, r_row;
+    long long y_row, gate_row, r_row, least_row;
     const void *y, *gate, *r;
     const float *w_post, *b_post, *scale, *w_pre, *b_pre;
     void *r_out, *o;
@@ -27,71 +26,526 @@ struct NormArgs {
     void *dy, *dr_in, *dgate;
     float* part;                 // [block][slot of sum][C]
     int slot[kSums], slots;      // which sums are wanted, and where; -1: not
+    bool wide, aligned;          // every tensor's rows have one phase; that phase is 0, and parameters are aligned
 };
 
-// Which column an element is: TPR threads hold V consecutive columns each, CH times over. Rows that are
-// not 16-byte aligned go column by column instead, neighbouring threads on neighbouring columns.
-template <int TPR, int V, bool WIDE>
-__device__ __forceinline__ int col_of(int k, int j, int tid) {
-    return WIDE ? (k * TPR + tid) * V + j : (k * V + j) * TPR + tid;
-}
-
-// V elements of type E (V * sizeof(E) = 16 or 32 bytes), wide.
-template <typename E, int V>
-__device__ __forceinline__ void ld_wide(const E* p, float (&v)[V]) {
-    if constexpr (V * sizeof(E) == 32) {
-        float a[V / 2], b[V / 2];
-        ld_lanes<E, V / 2>(p, a);
-        ld_lanes<E, V / 2>(p + V / 2, b);
+// ---------------------------------------------------------------------------- rows of up to 4096
+// How a row is held. E elements (8; 16 over 2048 columns, so that no block has over eight warps to sum
+// over) in each thread of a block of as many warps as the row needs, or of one warp where 32 E cover it: V consecutive columns (16 bytes) at a time, E / V times over, as E / 2
+// pairs. Rows of an odd number of columns start at other distances from a 16-byte border: the columns
+// of a thread are shifted by that phase, so that every full vector is still one aligned load. A block
+// takes rows of one phase only (the grid is a multiple of the phases' period), so a thread keeps its
+// columns, and with them its parameters and column sums. Vectors that cross an end of the row, and all
+// of a row whose tensors are aligned in different ways, go element by element.
+struct Row {
+    int C, tid, tpr, phase;
+    bool wide;
+};
+template <typename T, int E> struct Lay {
+    static constexpr int V = Vec<T>::V, H = E / 2, K = E / V;
+    static __device__ __forceinline__ int col(const Row& w, int e) { return (e / V * w.tpr + w.tid) * V + e % V - w.phase; }
+};
+// A row's elements of type S as stored, V columns (16 or 32 bytes, or 8) at a time.
+template <typename T, typename S, int E> struct RowRaw {
+    static constexpr int W = Vec<T>::V * sizeof(S) / 4;           // words of a vector
+    uint32_t q[E / Vec<T>::V][W];
+};
+// A vector that crosses an end of the row is loaded whole all the same, where its other columns are those
+// of rows around (before it they always are; `more`: seven elements follow behind the row too), and
+// those are set to zero.
+template <typename T, typename S, int E>
+__device__ __forceinline__ void ld_row(RowRaw<T, S, E>& r, const S* p, const Row& w, bool more) {
+    using Y = Lay<T, E>;
+    constexpr int V = Y::V, W = RowRaw<T, S, E>::W;
 #pragma unroll
-        for (int j = 0; j < V / 2; ++j) { v[j] = a[j]; v[j + V / 2] = b[j]; }
-    } else {
-        ld_lanes<E, V>(p, v);
-    }
-}
-template <typename E, int TPR, int CH, int V, bool WIDE>
-__device__ __forceinline__ void ld_row(const E* p, int C, int tid, float (&v)[CH][V]) {
-#pragma unroll
-    for (int k = 0; k < CH; ++k) {
-        if constexpr (WIDE) {
-            const int c = col_of<TPR, V, true>(k, 0, tid);
-            if (c < C) {
-                ld_wide<E, V>(p + c, v[k]);
+    for (int k = 0; k < Y::K; ++k) {
+        const int c = Y::col(w, k * V);
+        if (w.wide && c < w.C && (more || c + V <= w.C)) {
+            if constexpr (W == 2) {
+                const uint2 v = *(const uint2*)(p + c);
+                r.q[k][0] = v.x; r.q[k][1] = v.y;
             } else {
 #pragma unroll
-                for (int j = 0; j < V; ++j) v[k][j] = 0.f;
+                for (int m = 0; m < W; m += 4) {
+                    const uint4 v = *((const uint4*)(p + c) + m / 4);
+                    r.q[k][m] = v.x; r.q[k][m + 1] = v.y; r.q[k][m + 2] = v.z; r.q[k][m + 3] = v.w;
+                }
+            }
+            if (c < 0 || c + V > w.C) {
+#pragma unroll
+                for (int j = 0; j < W; ++j) {
+                    if constexpr (sizeof(S) == 4) {
+                        if (c + j < 0 || c + j >= w.C) r.q[k][j] = 0u;
+                    } else {
+                        const int c0 = c + 2 * j, c1 = c0 + 1;
+                        r.q[k][j] &= (c0 >= 0 && c0 < w.C ? 0xffffu : 0u) | (c1 >= 0 && c1 < w.C ? 0xffff0000u : 0u);
+                    }
+                }
             }
         } else {
 #pragma unroll
-            for (int j = 0; j < V; ++j) {
-                const int c = col_of<TPR, V, false>(k, j, tid);
-                v[k][j] = c < C ? Io<E>::ld(p + c) : 0.f;
+            for (int j = 0; j < W; ++j) {
+                if constexpr (sizeof(S) == 4) {
+                    const int cc = c + j;
+                    r.q[k][j] = cc >= 0 && cc < w.C ? ((const uint32_t*)p)[cc] : 0u;
+                } else {
+                    const int c0 = c + 2 * j, c1 = c0 + 1;
+                    const uint32_t lo = c0 >= 0 && c0 < w.C ? ((const uint16_t*)p)[c0] : 0u;
+                    const uint32_t hi = c1 >= 0 && c1 < w.C ? ((const uint16_t*)p)[c1] : 0u;
+                    r.q[k][j] = lo | hi << 16;
+                }
             }
         }
     }
 }
-template <typename E, int TPR, int CH, int V, bool WIDE>
-__device__ __forceinline__ void st_row(E* p, int C, int tid, const float (&v)[CH][V]) {
+template <typename T, typename S, int E>
+__device__ __forceinline__ void open_row(const RowRaw<T, S, E>& r, f2 (&v)[E / 2]) {
+    constexpr int W = RowRaw<T, S, E>::W;
 #pragma unroll
-    for (int k = 0; k < CH; ++k) {
-        if constexpr (WIDE) {
-            const int c = col_of<TPR, V, true>(k, 0, tid);
-            if (c < C) st_lanes<E, V>(p + c, v[k]);
+    for (int h = 0; h < E / 2; ++h) {
+        const int k = 2 * h / Vec<T>::V, at = 2 * h % Vec<T>::V;
+        if constexpr (sizeof(S) == 4) {
+            v[h] = pack(__uint_as_float(r.q[k][at]), __uint_as_float(r.q[k][at + 1]));
+        } else {
+            const uint32_t q = r.q[k][at / 2];
+            v[h] = pack(__uint_as_float(q << 16), __uint_as_float(q & 0xffff0000u));
+        }
+    }
+    (void)W;
+}
+template <typename T, typename S, int E>
+__device__ __forceinline__ void st_row(S* p, const Row& w, const f2 (&v)[E / 2]) {
+    using Y = Lay<T, E>;
+    constexpr int V = Y::V;
+#pragma unroll
+    for (int k = 0; k < Y::K; ++k) {
+        const int c = Y::col(w, k * V);
+        float f[V];
+        to_floats(*(const f2(*)[V / 2])(v + k * V / 2), f);
+        if (w.wide && c >= 0 && c + V <= w.C) {
+            st_lanes<S, V>(p + c, f);
         } else {
 #pragma unroll
-            for (int j = 0; j < V; ++j) {
-                const int c = col_of<TPR, V, false>(k, j, tid);
-                if (c < C) Io<E>::st(p + c, v[k][j]);
+            for (int j = 0; j < V; ++j)
+                if (c + j >= 0 && c + j < w.C) Io<S>::st(p + c + j, f[j]);
+        }
+    }
+}
+
+// The parameters of a thread's columns, zero where it has none, wait in shared memory, each thread's apart:
+// shifted columns are not aligned in global memory.
+enum { kWPost, kBPost, kScale, kWPre, kBPre, kParams };
+template <typename T, int E> struct Params {
+    float* at;                   // [parameter][E / 4][tpr][4]: neighbouring threads on neighbouring 16 bytes
+    int stride;
+    __device__ __forceinline__ void get(int i, const Row& w, f2 (&v)[E / 2]) const {
+#pragma unroll
+        for (int e = 0; e < E; e += 4)
+            ld_pairs(at + i * stride + (e / 4 * w.tpr + w.tid) * 4, v[e / 2], v[e / 2 + 1]);
+    }
+    __device__ __forceinline__ void put(int i, const float* p, const Row& w) {
+        if (!p) return;
+        using Y = Lay<T, E>;
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            const int c = Y::col(w, e);
+            at[i * stride + (e / 4 * w.tpr + w.tid) * 4 + e % 4] = c >= 0 && c < w.C ? p[c] : 0.f;
+        }
+    }
+};
+
+// Sums over the threads of a row: the lanes of a warp, or (WARP = false) the warps of the block as well.
+// Three buffers in turn, so that one barrier a call is enough.
+template <bool WARP>
+struct RowSum {
+    float (*buf)[2][32];
+    int turn = 0;
+    __device__ __forceinline__ float one(float a) {
+#pragma unroll
+        for (int o = 16; o; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
+        if constexpr (WARP) return a;
+        if ((threadIdx.x & 31) == 0) buf[turn][0][threadIdx.x >> 5] = a;
+        __syncthreads();
+        a = over_warps(0);
+        turn = turn == 2 ? 0 : turn + 1;
+        return a;
+    }
+    // two sums at once: half of the lanes go on with each
+    __device__ __forceinline__ float2 two(float a, float b) {
+        const bool up = threadIdx.x & 16;
+        float v = (up ? b : a) + __shfl_xor_sync(0xffffffffu, up ? a : b, 16);
+#pragma unroll
+        for (int o = 8; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+        if constexpr (WARP) {
+            const float w = __shfl_xor_sync(0xffffffffu, v, 16);
+            return up ? make_float2(w, v) : make_float2(v, w);
+        }
+        if ((threadIdx.x & 15) == 0) buf[turn][up][threadIdx.x >> 5] = v;
+        __syncthreads();
+        const float2 s = make_float2(over_warps(0), over_warps(1));
+        turn = turn == 2 ? 0 : turn + 1;
+        return s;
+    }
+    __device__ __forceinline__ float over_warps(int i) const {
+        const int warps = blockDim.x >> 5;
+        f2 s = both(0.f);
+        for (int w = 0; w < warps; w += 4) {                      // places behind the last warp hold zeros
+            f2 x, y;
+            ld_pairs(&buf[turn][i][w], x, y);
+            s = add2(s, add2(x, y));
+        }
+        const float2 v = unpack(s);
+        return v.x + v.y;
+    }
+};
+template <int H>
+__device__ __forceinline__ float sum_all(const f2 (&v)[H]) {
+    f2 s = v[0];
+#pragma unroll
+    for (int k = 1; k < H; ++k) s = add2(s, v[k]);
+    const float2 f = unpack(s);
+    return f.x + f.y;
+}
+template <int H>
+__device__ __forceinline__ float dot_all(const f2 (&v)[H], const f2 (&w)[H]) {
+    f2 s = mul2(v[0], w[0]);
+#pragma unroll
+    for (int k = 1; k < H; ++k) s = fma2(v[k], w[k], s);
+    const float2 f = unpack(s);
+    return f.x + f.y;
+}
+
+// Takes v to its normalised form in place; returns one over its spread.
+template <typename T, int E, bool WARP>
+__device__ __forceinline__ float to_unit(f2 (&v)[E / 2], const NormArgs& p, const Row& w, RowSum<WARP>& sum) {
+    using Y = Lay<T, E>;
+    if (p.center) {
+        const f2 mean = both(-sum.one(sum_all(v)) * p.inv_c);
+#pragma unroll
+        for (int k = 0; k < Y::K; ++k) {
+            const int c = Y::col(w, k * Y::V);
+            const bool inside = c >= 0 && c + Y::V <= w.C;
+#pragma unroll
+            for (int j = 0; j < Y::V; j += 2) {
+                f2& x = v[(k * Y::V + j) / 2];
+                x = add2(x, mean);
+                if (!inside) {                                    // places that are no columns stay zero
+                    const float2 f = unpack(x);
+                    x = pack(c + j >= 0 && c + j < w.C ? f.x : 0.f, c + j + 1 >= 0 && c + j + 1 < w.C ? f.y : 0.f);
+                }
+            }
+        }
+    }
+    const float rs = rsqrtf(fmaf(sum.one(dot_all(v, v)), p.inv_c, p.eps));
+#pragma unroll
+    for (int k = 0; k < E / 2; ++k) v[k] = mul2(v[k], both(rs));
+    return rs;
+}
+
+template <typename T, int E>
+__device__ __forceinline__ void scale_by(f2 (&v)[E / 2], const Params<T, E>& prm, int i, const Row& w) {
+    f2 t[E / 2];
+    prm.get(i, w, t);
+#pragma unroll
+    for (int k = 0; k < E / 2; ++k) v[k] = mul2(v[k], t[k]);
+}
+template <typename T, int E>
+__device__ __forceinline__ void scale_shift(f2 (&v)[E / 2], const Params<T, E>& prm, int i, bool shift, const Row& w) {
+    scale_by<T, E>(v, prm, i, w);
+    if (!shift) return;
+    f2 t[E / 2];
+    prm.get(i + 1, w, t);
+#pragma unroll
+    for (int k = 0; k < E / 2; ++k) v[k] = add2(v[k], t[k]);
+}
+
+// The block's place: its first row, the step to its next ones, and how it holds them.
+template <typename T, int E, bool WARP>
+__device__ __forceinline__ Row place(const NormArgs& p, long long& row, long long& step) {
+    Row w;
+    w.C = p.C;
+    w.tid = WARP ? threadIdx.x & 31 : threadIdx.x;
+    w.tpr = WARP ? 32 : blockDim.x;
+    row = WARP ? (long long)blockIdx.x * 4 + (threadIdx.x >> 5) : blockIdx.x;
+    step = WARP ? (long long)gridDim.x * 4 : gridDim.x;
+    w.wide = p.wide;
+    w.phase = p.wide ? (int)(row * p.C % Lay<T, E>::V) : 0;
+    return w;
+}
+template <typename T, int E, bool WARP>
+__device__ __forceinline__ Params<T, E> params(const NormArgs& p, const Row& w, float* smem, float (*buf)[2][32]) {
+    Params<T, E> q{smem + (WARP ? (threadIdx.x >> 5) * kParams * 32 * E : 0), w.tpr * E};
+    q.put(kWPost, p.w_post, w);
+    q.put(kBPost, p.b_post, w);
+    q.put(kScale, p.scale, w);
+    q.put(kWPre, p.w_pre, w);
+    q.put(kBPre, p.b_pre, w);
+    if constexpr (!WARP) {
+        if (threadIdx.x < 32)
+            for (int i = 0; i < 6; ++i) buf[i / 2][i % 2][threadIdx.x] = 0.f;
+        __syncthreads();
+    }
+    return q;
+}
+
+// MAXT: the most threads a block has; 128: four warps with a row each. The next row's loads are in flight
+// while the present one is worked on.
+template <typename T, typename R, int E, int MAXT, bool WARP = MAXT == 128>
+__global__ void __launch_bounds__(MAXT, MAXT == 128 ? 1 : E == 8 ? 4 : 2) k_norm_fwd(const NormArgs p) {
+    constexpr int H = E / 2;
+    __shared__ __align__(16) float buf[3][2][32];
+    extern __shared__ __align__(16) float smem[];
+    RowSum<WARP> sum{buf};
+    long long row, step;
+    const Row w = place<T, E, WARP>(p, row, step);
+    const Params<T, E> prm = params<T, E, WARP>(p, w, smem, buf);
+    RowRaw<T, T, E> ny{}, ng{};
+    RowRaw<T, R, E> nr{};
+    auto load = [&](long long r) {
+        const bool more = (p.rows - 1 - r) * p.least_row >= 7;
+        ld_row<T, T, E>(ny, (const T*)p.y + r * p.y_row, w, more);
+        if (p.r) ld_row<T, R, E>(nr, (const R*)p.r + r * p.r_row, w, more);
+        if (p.gate) ld_row<T, T, E>(ng, (const T*)p.gate + r * p.gate_row, w, more);
+    };
+    if (row < p.rows) load(row);
+    for (; row < p.rows; row += step) {
+        f2 m[H], r[H], g[H];
+        open_row<T, T, E>(ny, m);
+        open_row<T, R, E>(nr, r);
+        open_row<T, T, E>(ng, g);
+        if (row + step < p.rows) load(row + step);
+        if (p.gate) {
+#pragma unroll
+            for (int k = 0; k < H; ++k) m[k] = mul2(m[k], silu2(g[k]));
+        }
+        if (p.w_post) {
+            to_unit<T, E, WARP>(m, p, w, sum);
+            scale_shift<T, E>(m, prm, kWPost, p.b_post != nullptr, w);
+        }
+        if (p.scale) scale_by<T, E>(m, prm, kScale, w);
+#pragma unroll
+        for (int k = 0; k < H; ++k) r[k] = add2(r[k], m[k]);
+        st_row<T, R, E>((R*)p.r_out + row * p.C, w, r);
+        if (p.w_pre) {
+            to_unit<T, E, WARP>(r, p, w, sum);
+            scale_shift<T, E>(r, prm, kWPre, p.b_pre != nullptr, w);
+            st_row<T, T, E>((T*)p.o + row * p.C, w, r);
+        }
+    }
+}
+
+// Backward of one norm: g = gradient of its normalised form (already times the weight) is taken in
+// place to the gradient of its input: (g - unit mean(g unit) - mean(g)) / spread, the last mean only
+// when centred. Places that are no columns end up with -mean(g) / spread: the next weight is zero there,
+// and they are never stored.
+template <int H, bool WARP>
+__device__ __forceinline__ void unit_back(f2 (&g)[H], const f2 (&unit)[H], float rs, const NormArgs& p, RowSum<WARP>& sum) {
+    const float a = dot_all(g, unit);
+    const float2 s = p.center ? sum.two(a, sum_all(g)) : make_float2(sum.one(a), 0.f);
+    const f2 ma = both(-s.x * p.inv_c), mb = both(-s.y * p.inv_c), k2 = both(rs);
+#pragma unroll
+    for (int k = 0; k < H; ++k) g[k] = mul2(add2(g[k], fma2(unit[k], ma, mb)), k2);
+}
+
+// Column sums over the rows of a block, in registers: a thread's columns are its own.
+template <int H> struct Cols {
+    f2 v[kSums * H];
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int i = 0; i < kSums * H; ++i) v[i] = both(0.f);
+    }
+    template <int WHICH> __device__ __forceinline__ void add(int slot, const f2 (&x)[H]) {
+        if (slot < 0) return;
+#pragma unroll
+        for (int k = 0; k < H; ++k) v[WHICH * H + k] = add2(v[WHICH * H + k], x[k]);
+    }
+    template <int WHICH> __device__ __forceinline__ void add_product(int slot, const f2 (&x)[H], const f2 (&y)[H]) {
+        if (slot < 0) return;
+#pragma unroll
+        for (int k = 0; k < H; ++k) v[WHICH * H + k] = fma2(x[k], y[k], v[WHICH * H + k]);
+    }
+};
+
+// One block takes rows blockIdx, blockIdx + grid, ... (four at a time, one a warp, where a warp holds a
+// row) and keeps its column sums until the end; k_norm_sum adds the blocks in order.
+template <typename T, typename R, int E, int MAXT, bool WARP = MAXT == 128>
+__global__ void __launch_bounds__(MAXT, MAXT == 256 && E == 8 ? 2 : 1) k_norm_bwd(const NormArgs p) {
+    using Y = Lay<T, E>;
+    constexpr int H = E / 2;
+    __shared__ __align__(16) float buf[3][2][32];
+    extern __shared__ __align__(16) float smem[];
+    RowSum<WARP> sum{buf};
+    long long row, step;
+    const Row w = place<T, E, WARP>(p, row, step);
+    const Params<T, E> prm = params<T, E, WARP>(p, w, smem, buf);
+    Cols<H> cols;
+    cols.clear();
+    RowRaw<T, T, E> ny{}, ng{}, no{};
+    RowRaw<T, R, E> nu{}, nd{};
+    auto load = [&](long long r) {
+        const bool more = (p.rows - 1 - r) * p.least_row >= 7;
+        ld_row<T, T, E>(ny, (const T*)p.y + r * p.y_row, w, more);
+        if (p.gate) ld_row<T, T, E>(ng, (const T*)p.gate + r * p.gate_row, w, more);
+        if (p.w_pre) {
+            ld_row<T, R, E>(nu, (const R*)p.r + r * p.r_row, w, more);
+            ld_row<T, T, E>(no, (const T*)p.go + r * p.C, w, more);
+        }
+        if (p.dr) ld_row<T, R, E>(nd, (const R*)p.dr + r * p.C, w, more);
+    };
+    if (row < p.rows) load(row);
+    for (; row < p.rows; row += step) {
+        f2 d[H], y[H], g[H];                                      // d: the gradient of r_out
+        f2 u[H], go[H];
+        open_row<T, T, E>(ny, y);
+        open_row<T, T, E>(ng, g);
+        open_row<T, R, E>(nd, d);
+        open_row<T, R, E>(nu, u);
+        open_row<T, T, E>(no, go);
+        if (row + step < p.rows) load(row + step);
+        if (p.w_pre) {
+            const float rs = to_unit<T, E, WARP>(u, p, w, sum);
+            cols.template add<kDbPre>(p.slot[kDbPre], go);
+            cols.template add_product<kDwPre>(p.slot[kDwPre], go, u);
+            scale_by<T, E>(go, prm, kWPre, w);
+            unit_back<H, WARP>(go, u, rs, p, sum);
+#pragma unroll
+            for (int k = 0; k < H; ++k) d[k] = add2(d[k], go[k]);
+        }
+        if (p.dr_in) st_row<T, R, E>((R*)p.dr_in + row * p.C, w, d);
+        f2 m[H], s[H];
+#pragma unroll
+        for (int k = 0; k < H; ++k) {
+            if (p.gate) s[k] = sigmoid2(g[k]);
+            m[k] = p.gate ? mul2(y[k], mul2(g[k], s[k])) : y[k];
+        }
+        float rs = 1.f;
+        if (p.w_post) rs = to_unit<T, E, WARP>(m, p, w, sum);
+        if (p.slot[kDscale] >= 0) {
+            f2 v[H];
+#pragma unroll
+            for (int k = 0; k < H; ++k) v[k] = m[k];
+            if (p.w_post) scale_shift<T, E>(v, prm, kWPost, p.b_post != nullptr, w);
+            cols.template add_product<kDscale>(p.slot[kDscale], v, d);
+        }
+        if (p.scale) scale_by<T, E>(d, prm, kScale, w);
+        if (p.w_post) {
+            cols.template add<kDbPost>(p.slot[kDbPost], d);
+            cols.template add_product<kDwPost>(p.slot[kDwPost], d, m);
+            scale_by<T, E>(d, prm, kWPost, w);
+            unit_back<H, WARP>(d, m, rs, p, sum);
+        }
+        if (p.gate) {
+            if (p.dgate) {
+                f2 o[H];
+#pragma unroll
+                for (int k = 0; k < H; ++k)                       // slope of silu: s + g s (1 - s)
+                    o[k] = mul2(mul2(d[k], y[k]), fma2(mul2(g[k], s[k]), fma2(s[k], both(-1.f), both(1.f)), s[k]));
+                st_row<T, T, E>((T*)p.dgate + row * p.C, w, o);
+            }
+#pragma unroll
+            for (int k = 0; k < H; ++k) d[k] = mul2(d[k], mul2(g[k], s[k]));
+        }
+        st_row<T, T, E>((T*)p.dy + row * p.C, w, d);
+    }
+    // this block's sums: [sum][C]
+    float* part = p.part + (long long)blockIdx.x * p.slots * p.C;
+    if constexpr (WARP) {
+        // the four warps' sums in order, one sum at a time through shared memory
+        float (*red)[32 * E] = (float(*)[32 * E])smem;
+#pragma unroll
+        for (int i = 0; i < kSums; ++i) {
+            if (p.slot[i] < 0) continue;
+            __syncthreads();
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                const float2 f = unpack(cols.v[i * H + e / 2]);
+                const int c = Y::col(w, e);
+                if (c >= 0 && c < p.C) red[threadIdx.x >> 5][c] = e & 1 ? f.y : f.x;
+            }
+            __syncthreads();
+            for (int c = threadIdx.x; c < p.C; c += blockDim.x)
+                part[p.slot[i] * p.C + c] = (red[0][c] + red[1][c]) + (red[2][c] + red[3][c]);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < kSums; ++i) {
+            if (p.slot[i] < 0) continue;
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                const int c = Y::col(w, e);
+                const float2 f = unpack(cols.v[i * H + e / 2]);
+                if (c >= 0 && c < p.C) part[p.slot[i] * p.C + c] = e & 1 ? f.y : f.x;
             }
         }
     }
 }
 
-// Sum of a and b over the TPR threads of a row. `buf`: two floats for each warp, a fresh one each call
-// in turn of three, so that one barrier a call is enough.
-template <int TPR>
-struct RowSum {
-    float2 (*buf)[TPR / 32];
+// ------------------------------------------------------------------------------------ wide rows
+// Rows of over 4096 columns: 16 elements in each thread of a block of as many warps as the row needs.
+// ALIGNED: V consecutive columns (16 bytes) at a time; a row that is not 16-byte aligned goes column by
+// column instead, neighbouring threads on neighbouring columns. Parameters are read again for every row
+// and column sums wait in shared memory: neither fits the registers.
+template <typename T, int E, bool ALIGNED> struct WideLay {
+    static constexpr int V = Vec<T>::V, H = E / 2;
+    static __device__ __forceinline__ int col(int e, int tid, int tpr) {
+        return ALIGNED ? (e / V * tpr + tid) * V + e % V : e * tpr + tid;
+    }
+};
+
+// Reads the thread's columns of a row of elements S (T, the residual's type, or fp32 parameters).
+template <typename T, typename S, int E, bool ALIGNED>
+__device__ __forceinline__ void wide_ld_row(const S* p, int C, int tid, int tpr, f2 (&v)[E / 2]) {
+    using Y = WideLay<T, E, ALIGNED>;
+    if constexpr (ALIGNED) {
+        constexpr int V = Y::V, Q = 16 / sizeof(S);               // columns of a vector; of a 16-byte load
+#pragma unroll
+        for (int k = 0; k < E / V; ++k) {
+            const int c = Y::col(k * V, tid, tpr);
+#pragma unroll
+            for (int m = 0; m < V; m += (Q < V ? Q : V)) {
+                if constexpr (Q <= V) {
+                    const uint4 q = c < C ? *(const uint4*)(p + c + m) : make_uint4(0, 0, 0, 0);
+                    to_pairs(q, *(f2(*)[Q / 2])(v + (k * V + m) / 2));
+                } else {
+                    const uint2 q = c < C ? *(const uint2*)(p + c) : make_uint2(0, 0);
+                    to_pairs(q, *(f2(*)[2])(v + k * V / 2));
+                }
+            }
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < E; e += 2) {
+            const int c0 = Y::col(e, tid, tpr), c1 = Y::col(e + 1, tid, tpr);
+            v[e / 2] = pack(c0 < C ? Io<S>::ld(p + c0) : 0.f, c1 < C ? Io<S>::ld(p + c1) : 0.f);
+        }
+    }
+}
+template <typename T, typename S, int E, bool ALIGNED>
+__device__ __forceinline__ void wide_st_row(S* p, int C, int tid, int tpr, const f2 (&v)[E / 2]) {
+    using Y = WideLay<T, E, ALIGNED>;
+    if constexpr (ALIGNED) {
+        constexpr int V = Y::V;
+#pragma unroll
+        for (int k = 0; k < E / V; ++k) {
+            const int c = Y::col(k * V, tid, tpr);
+            float f[V];
+            to_floats(*(const f2(*)[V / 2])(v + k * V / 2), f);
+            if (c < C) st_lanes<S, V>(p + c, f);
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < E; e += 2) {
+            const float2 f = unpack(v[e / 2]);
+            const int c0 = Y::col(e, tid, tpr), c1 = Y::col(e + 1, tid, tpr);
+            if (c0 < C) Io<S>::st(p + c0, f.x);
+            if (c1 < C) Io<S>::st(p + c1, f.y);
+        }
+    }
+}
+
+// Sums of a and b over the threads of a block, three buffers in turn so that one barrier a call is enough.
+struct WideSum {
+    float2 (*buf)[32];
     int turn = 0;
     __device__ __forceinline__ float2 operator()(float a, float b) {
 #pragma unroll
@@ -99,284 +553,213 @@ struct RowSum {
             a += __shfl_xor_sync(0xffffffffu, a, o);
             b += __shfl_xor_sync(0xffffffffu, b, o);
         }
-        if constexpr (TPR == 32) {
-            return make_float2(a, b);
-        } else {
-            const int w = threadIdx.x >> 5;
-            if ((threadIdx.x & 31) == 0) buf[turn][w] = make_float2(a, b);
-            __syncthreads();
-            float2 s = make_float2(0.f, 0.f);
+        if ((threadIdx.x & 31) == 0) buf[turn][threadIdx.x >> 5] = make_float2(a, b);
+        __syncthreads();
+        const int warps = blockDim.x >> 5, lane = threadIdx.x & 31;
+        float2 s = lane < warps ? buf[turn][lane] : make_float2(0.f, 0.f);
 #pragma unroll
-            for (int i = 0; i < TPR / 32; ++i) {
-                const float2 v = buf[turn][i];
-                s.x += v.x;
-                s.y += v.y;
-            }
-            turn = turn == 2 ? 0 : turn + 1;
-            return s;
+        for (int o = 16; o; o >>= 1) {
+            s.x += __shfl_xor_sync(0xffffffffu, s.x, o);
+            s.y += __shfl_xor_sync(0xffffffffu, s.y, o);
         }
+        turn = turn == 2 ? 0 : turn + 1;
+        return s;
     }
 };
 
 // Takes v to its normalised form in place; returns one over its spread.
-template <int TPR, int CH, int V, bool WIDE>
-__device__ __forceinline__ float to_unit(float (&v)[CH][V], const NormArgs& p, int tid, RowSum<TPR>& sum) {
+template <typename T, int E, bool ALIGNED>
+__device__ __forceinline__ float wide_to_unit(f2 (&v)[E / 2], const NormArgs& p, int tid, int tpr, WideSum& sum) {
+    using Y = WideLay<T, E, ALIGNED>;
     if (p.center) {
-        float s = 0.f;
+        const f2 mean = both(-sum(sum_all(v), 0.f).x * p.inv_c);
 #pragma unroll
-        for (int k = 0; k < CH; ++k)
-#pragma unroll
-            for (int j = 0; j < V; ++j) s += v[k][j];
-        const float mean = sum(s, 0.f).x * p.inv_c;
-#pragma unroll
-        for (int k = 0; k < CH; ++k)
-#pragma unroll
-            for (int j = 0; j < V; ++j) v[k][j] = col_of<TPR, V, WIDE>(k, j, tid) < p.C ? v[k][j] - mean : 0.f;
+        for (int k = 0; k < E / 2; ++k) {
+            const float2 f = unpack(add2(v[k], mean));
+            v[k] = pack(Y::col(2 * k, tid, tpr) < p.C ? f.x : 0.f, Y::col(2 * k + 1, tid, tpr) < p.C ? f.y : 0.f);
+        }
     }
-    float s = 0.f;
+    const float rs = rsqrtf(fmaf(sum(dot_all(v, v), 0.f).x, p.inv_c, p.eps));
 #pragma unroll
-    for (int k = 0; k < CH; ++k)
-#pragma unroll
-        for (int j = 0; j < V; ++j) s = fmaf(v[k][j], v[k][j], s);
-    const float rs = rsqrtf(fmaf(sum(s, 0.f).x, p.inv_c, p.eps));
-#pragma unroll
-    for (int k = 0; k < CH; ++k)
-#pragma unroll
-        for (int j = 0; j < V; ++j) v[k][j] *= rs;
+    for (int k = 0; k < E / 2; ++k) v[k] = mul2(v[k], both(rs));
     return rs;
 }
 
 // v w + b for the columns of this thread.
-template <int TPR, int CH, int V, bool WIDE>
-__device__ __forceinline__ void scale_shift(float (&v)[CH][V], const float* w, const float* b, int C, int tid) {
-    float t[CH][V];
-    ld_row<float, TPR, CH, V, WIDE>(w, C, tid, t);
+template <typename T, int E, bool ALIGNED>
+__device__ __forceinline__ void wide_scale_shift(f2 (&v)[E / 2], const float* w, const float* b, int C, int tid, int tpr) {
+    f2 t[E / 2];
+    wide_ld_row<T, float, E, ALIGNED>(w, C, tid, tpr, t);
 #pragma unroll
-    for (int k = 0; k < CH; ++k)
-#pragma unroll
-        for (int j = 0; j < V; ++j) v[k][j] *= t[k][j];
+    for (int k = 0; k < E / 2; ++k) v[k] = mul2(v[k], t[k]);
     if (!b) return;
-    ld_row<float, TPR, CH, V, WIDE>(b, C, tid, t);
+    wide_ld_row<T, float, E, ALIGNED>(b, C, tid, tpr, t);
 #pragma unroll
-    for (int k = 0; k < CH; ++k)
-#pragma unroll
-        for (int j = 0; j < V; ++j) v[k][j] += t[k][j];
+    for (int k = 0; k < E / 2; ++k) v[k] = add2(v[k], t[k]);
 }
 
-template <typename T, typename R, int TPR, int CH, bool WIDE>
-__global__ void __launch_bounds__(TPR == 32 ? 128 : TPR) k_norm_fwd(const NormArgs p) {
-    constexpr int V = Vec<T>::V, RPB = TPR == 32 ? 4 : 1;
-    __shared__ float2 buf[3][TPR / 32];
-    RowSum<TPR> sum{buf};
-    const int tid = TPR == 32 ? threadIdx.x & 31 : threadIdx.x;
-    const long long row = (long long)blockIdx.x * RPB + (TPR == 32 ? threadIdx.x >> 5 : 0);
-    if (row >= p.rows) return;               // whole warps only where RPB > 1; no barrier is used there
-    float m[CH][V], r[CH][V];
-    ld_row<T, TPR, CH, V, WIDE>((const T*)p.y + row * p.y_row, p.C, tid, m);
-    if (p.r) {
-        ld_row<R, TPR, CH, V, WIDE>((const R*)p.r + row * p.r_row, p.C, tid, r);
-    } else {
+template <typename T, typename R, int E, bool ALIGNED, int MAXT>
+__global__ void __launch_bounds__(MAXT, 1) k_norm_fwd_wide(const NormArgs p) {
+    constexpr int H = E / 2;
+    __shared__ float2 buf[3][32];
+    WideSum sum{buf};
+    const int tid = threadIdx.x, tpr = blockDim.x;
+    const long long row = blockIdx.x;
+    f2 m[H], r[H];
+    wide_ld_row<T, T, E, ALIGNED>((const T*)p.y + row * p.y_row, p.C, tid, tpr, m);
 #pragma unroll
-        for (int k = 0; k < CH; ++k)
-#pragma unroll
-            for (int j = 0; j < V; ++j) r[k][j] = 0.f;
-    }
+    for (int k = 0; k < H; ++k) r[k] = both(0.f);
+    if (p.r) wide_ld_row<T, R, E, ALIGNED>((const R*)p.r + row * p.r_row, p.C, tid, tpr, r);
     if (p.gate) {
-        float g[CH][V];
-        ld_row<T, TPR, CH, V, WIDE>((const T*)p.gate + row * p.gate_row, p.C, tid, g);
+        f2 g[H];
+        wide_ld_row<T, T, E, ALIGNED>((const T*)p.gate + row * p.gate_row, p.C, tid, tpr, g);
 #pragma unroll
-        for (int k = 0; k < CH; ++k)
-#pragma unroll
-            for (int j = 0; j < V; ++j) m[k][j] *= silu(g[k][j]);
+        for (int k = 0; k < H; ++k) m[k] = mul2(m[k], silu2(g[k]));
     }
     if (p.w_post) {
-        to_unit<TPR, CH, V, WIDE>(m, p, tid, sum);
-        scale_shift<TPR, CH, V, WIDE>(m, p.w_post, p.b_post, p.C, tid);
+        wide_to_unit<T, E, ALIGNED>(m, p, tid, tpr, sum);
+        wide_scale_shift<T, E, ALIGNED>(m, p.w_post, p.b_post, p.C, tid, tpr);
     }
-    if (p.scale) scale_shift<TPR, CH, V, WIDE>(m, p.scale, nullptr, p.C, tid);
+    if (p.scale) wide_scale_shift<T, E, ALIGNED>(m, p.scale, nullptr, p.C, tid, tpr);
 #pragma unroll
-    for (int k = 0; k < CH; ++k)
-#pragma unroll
-        for (int j = 0; j < V; ++j) r[k][j] += m[k][j];
-    st_row<R, TPR, CH, V, WIDE>((R*)p.r_out + row * p.C, p.C, tid, r);
+    for (int k = 0; k < H; ++k) r[k] = add2(r[k], m[k]);
+    wide_st_row<T, R, E, ALIGNED>((R*)p.r_out + row * p.C, p.C, tid, tpr, r);
     if (p.w_pre) {
-        to_unit<TPR, CH, V, WIDE>(r, p, tid, sum);
-        scale_shift<TPR, CH, V, WIDE>(r, p.w_pre, p.b_pre, p.C, tid);
-        st_row<T, TPR, CH, V, WIDE>((T*)p.o + row * p.C, p.C, tid, r);
+        wide_to_unit<T, E, ALIGNED>(r, p, tid, tpr, sum);
+        wide_scale_shift<T, E, ALIGNED>(r, p.w_pre, p.b_pre, p.C, tid, tpr);
+        wide_st_row<T, T, E, ALIGNED>((T*)p.o + row * p.C, p.C, tid, tpr, r);
     }
 }
 
-// Backward of one norm: g = gradient of its normalised form (already times the weight) is taken in
-// place to the gradient of its input: (g - unit mean(g unit) - mean(g)) / spread, the last mean only
-// when centred.
-template <int TPR, int CH, int V, bool WIDE>
-__device__ __forceinline__ void unit_back(float (&g)[CH][V], const float (&unit)[CH][V], float rs, const NormArgs& p,
-                                          int tid, RowSum<TPR>& sum) {
-    float a = 0.f, b = 0.f;
+template <int H>
+__device__ __forceinline__ void wide_unit_back(f2 (&g)[H], const f2 (&unit)[H], float rs, const NormArgs& p, WideSum& sum) {
+    const float2 s = sum(dot_all(g, unit), p.center ? sum_all(g) : 0.f);
+    const f2 ma = both(-s.x * p.inv_c), mb = both(-s.y * p.inv_c), k2 = both(rs);
 #pragma unroll
-    for (int k = 0; k < CH; ++k)
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
-            a = fmaf(g[k][j], unit[k][j], a);
-            b += g[k][j];
-        }
-    const float2 s = sum(a, b);
-    const float ma = s.x * p.inv_c, mb = p.center ? s.y * p.inv_c : 0.f;
-#pragma unroll
-    for (int k = 0; k < CH; ++k)
-#pragma unroll
-        for (int j = 0; j < V; ++j) g[k][j] = (g[k][j] - fmaf(unit[k][j], ma, mb)) * rs;
+    for (int k = 0; k < H; ++k) g[k] = mul2(add2(g[k], fma2(unit[k], ma, mb)), k2);
 }
 
-// Adds this row's share of a column sum. A thread's columns of `acc` are its own.
-template <int TPR, int CH, int V, bool WIDE>
-__device__ __forceinline__ void add_cols(float* acc, int slot, int C, int tid, const float (&v)[CH][V]) {
-    if (slot < 0) return;
-    float* a = acc + (long long)slot * C;
-#pragma unroll
-    for (int k = 0; k < CH; ++k) {
-        if constexpr (WIDE) {
-            const int c = col_of<TPR, V, true>(k, 0, tid);
-            if (c < C) {
-#pragma unroll
-                for (int j = 0; j < V; j += 4) {
-                    float4 f = *(float4*)(a + c + j);
-                    f.x += v[k][j]; f.y += v[k][j + 1]; f.z += v[k][j + 2]; f.w += v[k][j + 3];
-                    *(float4*)(a + c + j) = f;
-                }
-            }
-        } else {
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-                const int c = col_of<TPR, V, false>(k, j, tid);
-                if (c < C) a[c] += v[k][j];
-            }
-        }
+// Column sums over the rows of a block, [sum][pair][thread]: a thread's columns are its own.
+template <int H> struct WideCols {
+    f2* at;
+    int tpr;
+    __device__ __forceinline__ void clear(int wanted) {
+        for (int i = 0; i < wanted * H; ++i) at[i * tpr] = both(0.f);
     }
-}
+    __device__ __forceinline__ void add(int slot, const f2 (&x)[H]) {
+        if (slot < 0) return;
+#pragma unroll
+        for (int k = 0; k < H; ++k) at[(slot * H + k) * tpr] = add2(at[(slot * H + k) * tpr], x[k]);
+    }
+    __device__ __forceinline__ void add_product(int slot, const f2 (&x)[H], const f2 (&y)[H]) {
+        if (slot < 0) return;
+#pragma unroll
+        for (int k = 0; k < H; ++k) at[(slot * H + k) * tpr] = fma2(x[k], y[k], at[(slot * H + k) * tpr]);
+    }
+};
 
-// One block takes rows blockIdx, blockIdx + grid, ... and keeps its column sums in shared memory, each
-// column in the hands of one thread; narrow rows have one set of sums for each of the four warps,
-// added in order at the end. k_norm_sum adds the blocks in order.
-template <typename T, typename R, int TPR, int CH, bool WIDE>
-__global__ void __launch_bounds__(TPR == 32 ? 128 : TPR) k_norm_bwd(const NormArgs p) {
-    constexpr int V = Vec<T>::V, RPB = TPR == 32 ? 4 : 1;
-    __shared__ float2 buf[3][TPR / 32];
-    extern __shared__ __align__(16) float acc_all[];
-    RowSum<TPR> sum{buf};
-    const int tid = TPR == 32 ? threadIdx.x & 31 : threadIdx.x;
-    const int grp = TPR == 32 ? threadIdx.x >> 5 : 0;
-    const int n = p.slots * p.C;
-    for (int i = threadIdx.x; i < RPB * n; i += blockDim.x) acc_all[i] = 0.f;
-    __syncthreads();
-    float* acc = acc_all + grp * n;
-    for (long long row = (long long)blockIdx.x * RPB + grp; row < p.rows; row += (long long)gridDim.x * RPB) {
-        float d[CH][V];                       // the gradient of r_out
-        if (p.dr) {
-            ld_row<R, TPR, CH, V, WIDE>((const R*)p.dr + row * p.C, p.C, tid, d);
-        } else {
-#pragma unroll
-            for (int k = 0; k < CH; ++k)
-#pragma unroll
-                for (int j = 0; j < V; ++j) d[k][j] = 0.f;
-        }
-        float m[CH][V], g[CH][V], y[CH][V];
-        ld_row<T, TPR, CH, V, WIDE>((const T*)p.y + row * p.y_row, p.C, tid, y);
-        if (p.gate) ld_row<T, TPR, CH, V, WIDE>((const T*)p.gate + row * p.gate_row, p.C, tid, g);
+// One block takes rows blockIdx, blockIdx + grid, ... and keeps its column sums until the end.
+template <typename T, typename R, int E, bool ALIGNED, int MAXT>
+__global__ void __launch_bounds__(MAXT, 1) k_norm_bwd_wide(const NormArgs p) {
+    using Y = WideLay<T, E, ALIGNED>;
+    constexpr int H = E / 2;
+    __shared__ float2 buf[3][32];
+    extern __shared__ __align__(16) unsigned char smem_raw[];
+    WideSum sum{buf};
+    const int tid = threadIdx.x, tpr = blockDim.x;
+    WideCols<H> cols;
+    cols.at = (f2*)smem_raw + tid;
+    cols.tpr = tpr;
+    cols.clear(p.slots);
+    for (long long row = blockIdx.x; row < p.rows; row += gridDim.x) {
+        f2 d[H], y[H], g[H], u[H], go[H];                         // d: the gradient of r_out
+        wide_ld_row<T, T, E, ALIGNED>((const T*)p.y + row * p.y_row, p.C, tid, tpr, y);
+        if (p.gate) wide_ld_row<T, T, E, ALIGNED>((const T*)p.gate + row * p.gate_row, p.C, tid, tpr, g);
         if (p.w_pre) {
-            float u[CH][V], go[CH][V];
-            ld_row<R, TPR, CH, V, WIDE>((const R*)p.r + row * p.r_row, p.C, tid, u);
-            ld_row<T, TPR, CH, V, WIDE>((const T*)p.go + row * p.C, p.C, tid, go);
-            const float rs = to_unit<TPR, CH, V, WIDE>(u, p, tid, sum);
-            add_cols<TPR, CH, V, WIDE>(acc, p.slot[kDbPre], p.C, tid, go);
-            float t[CH][V];
-#pragma unroll
-            for (int k = 0; k < CH; ++k)
-#pragma unroll
-                for (int j = 0; j < V; ++j) t[k][j] = go[k][j] * u[k][j];
-            add_cols<TPR, CH, V, WIDE>(acc, p.slot[kDwPre], p.C, tid, t);
-            scale_shift<TPR, CH, V, WIDE>(go, p.w_pre, nullptr, p.C, tid);
-            unit_back<TPR, CH, V, WIDE>(go, u, rs, p, tid, sum);
-#pragma unroll
-            for (int k = 0; k < CH; ++k)
-#pragma unroll
-                for (int j = 0; j < V; ++j) d[k][j] += go[k][j];
+            wide_ld_row<T, R, E, ALIGNED>((const R*)p.r + row * p.r_row, p.C, tid, tpr, u);
+            wide_ld_row<T, T, E, ALIGNED>((const T*)p.go + row * p.C, p.C, tid, tpr, go);
         }
-        if (p.dr_in) st_row<R, TPR, CH, V, WIDE>((R*)p.dr_in + row * p.C, p.C, tid, d);
 #pragma unroll
-        for (int k = 0; k < CH; ++k)
+        for (int k = 0; k < H; ++k) d[k] = both(0.f);
+        if (p.dr) wide_ld_row<T, R, E, ALIGNED>((const R*)p.dr + row * p.C, p.C, tid, tpr, d);
+        if (p.w_pre) {
+            const float rs = wide_to_unit<T, E, ALIGNED>(u, p, tid, tpr, sum);
+            cols.add(p.slot[kDbPre], go);
+            cols.add_product(p.slot[kDwPre], go, u);
+            wide_scale_shift<T, E, ALIGNED>(go, p.w_pre, nullptr, p.C, tid, tpr);
+            wide_unit_back<H>(go, u, rs, p, sum);
 #pragma unroll
-            for (int j = 0; j < V; ++j) m[k][j] = p.gate ? y[k][j] * silu(g[k][j]) : y[k][j];
+            for (int k = 0; k < H; ++k) d[k] = add2(d[k], go[k]);
+        }
+        if (p.dr_in) wide_st_row<T, R, E, ALIGNED>((R*)p.dr_in + row * p.C, p.C, tid, tpr, d);
+        f2 m[H], s[H];
+#pragma unroll
+        for (int k = 0; k < H; ++k) {
+            if (p.gate) s[k] = sigmoid2(g[k]);
+            m[k] = p.gate ? mul2(y[k], mul2(g[k], s[k])) : y[k];
+        }
         float rs = 1.f;
-        if (p.w_post) rs = to_unit<TPR, CH, V, WIDE>(m, p, tid, sum);
+        if (p.w_post) rs = wide_to_unit<T, E, ALIGNED>(m, p, tid, tpr, sum);
         if (p.slot[kDscale] >= 0) {
-            float v[CH][V];
+            f2 v[H];
 #pragma unroll
-            for (int k = 0; k < CH; ++k)
-#pragma unroll
-                for (int j = 0; j < V; ++j) v[k][j] = m[k][j];
-            if (p.w_post) scale_shift<TPR, CH, V, WIDE>(v, p.w_post, p.b_post, p.C, tid);
-#pragma unroll
-            for (int k = 0; k < CH; ++k)
-#pragma unroll
-                for (int j = 0; j < V; ++j) v[k][j] *= d[k][j];
-            add_cols<TPR, CH, V, WIDE>(acc, p.slot[kDscale], p.C, tid, v);
+            for (int k = 0; k < H; ++k) v[k] = m[k];
+            if (p.w_post) wide_scale_shift<T, E, ALIGNED>(v, p.w_post, p.b_post, p.C, tid, tpr);
+            cols.add_product(p.slot[kDscale], v, d);
         }
-        if (p.scale) scale_shift<TPR, CH, V, WIDE>(d, p.scale, nullptr, p.C, tid);
+        if (p.scale) wide_scale_shift<T, E, ALIGNED>(d, p.scale, nullptr, p.C, tid, tpr);
         if (p.w_post) {
-            add_cols<TPR, CH, V, WIDE>(acc, p.slot[kDbPost], p.C, tid, d);
-            if (p.slot[kDwPost] >= 0) {
-                float t[CH][V];
-#pragma unroll
-                for (int k = 0; k < CH; ++k)
-#pragma unroll
-                    for (int j = 0; j < V; ++j) t[k][j] = d[k][j] * m[k][j];
-                add_cols<TPR, CH, V, WIDE>(acc, p.slot[kDwPost], p.C, tid, t);
-            }
-            scale_shift<TPR, CH, V, WIDE>(d, p.w_post, nullptr, p.C, tid);
-            unit_back<TPR, CH, V, WIDE>(d, m, rs, p, tid, sum);
+            cols.add(p.slot[kDbPost], d);
+            cols.add_product(p.slot[kDwPost], d, m);
+            wide_scale_shift<T, E, ALIGNED>(d, p.w_post, nullptr, p.C, tid, tpr);
+            wide_unit_back<H>(d, m, rs, p, sum);
         }
         if (p.gate) {
             if (p.dgate) {
-                float t[CH][V];
+                f2 o[H];
 #pragma unroll
-                for (int k = 0; k < CH; ++k)
-#pragma unroll
-                    for (int j = 0; j < V; ++j) t[k][j] = d[k][j] * y[k][j] * silu_slope(g[k][j]);
-                st_row<T, TPR, CH, V, WIDE>((T*)p.dgate + row * p.C, p.C, tid, t);
+                for (int k = 0; k < H; ++k)                       // slope of silu: s + g s (1 - s)
+                    o[k] = mul2(mul2(d[k], y[k]), fma2(mul2(g[k], s[k]), fma2(s[k], both(-1.f), both(1.f)), s[k]));
+                wide_st_row<T, T, E, ALIGNED>((T*)p.dgate + row * p.C, p.C, tid, tpr, o);
             }
 #pragma unroll
-            for (int k = 0; k < CH; ++k)
-#pragma unroll
-                for (int j = 0; j < V; ++j) d[k][j] *= silu(g[k][j]);
+            for (int k = 0; k < H; ++k) d[k] = mul2(d[k], mul2(g[k], s[k]));
         }
-        st_row<T, TPR, CH, V, WIDE>((T*)p.dy + row * p.C, p.C, tid, d);
+        wide_st_row<T, T, E, ALIGNED>((T*)p.dy + row * p.C, p.C, tid, tpr, d);
     }
-    __syncthreads();
-    for (int i = threadIdx.x; i < n; i += blockDim.x) {
-        float s = 0.f;
+    // this block's sums: [sum][C]
+    float* part = p.part + (long long)blockIdx.x * p.slots * p.C;
 #pragma unroll
-        for (int w = 0; w < RPB; ++w) s += acc_all[w * n + i];
-        p.part[(long long)blockIdx.x * n + i] = s;
+    for (int w = 0; w < kSums; ++w) {
+        if (p.slot[w] < 0) continue;
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            const int c = Y::col(e, tid, tpr);
+            const float2 f = unpack(cols.at[(p.slot[w] * H + e / 2) * tpr]);
+            if (c < p.C) part[p.slot[w] * p.C + c] = e & 1 ? f.y : f.x;
+        }
     }
 }
 
 struct SumOut {
     float* to[kSums];
 };
-// The blocks' column sums in order: 32 columns a block, 8 rows of threads share the blocks.
+// The blocks' column sums: 32 columns a block, each by 16 threads that take every 16th block; their sums
+// are added in order.
 __global__ void k_norm_sum(const float* part, int blocks, int n, int C, SumOut out) {
-    __shared__ float red[8][32];
+    __shared__ float red[16][32];
     const int i = blockIdx.x * 32 + threadIdx.x;
     float s = 0.f;
-    if (i < n)
-        for (int b = threadIdx.y; b < blocks; b += 8) s += part[(long long)b * n + i];
+    if (i < n) {
+#pragma unroll 8
+        for (int b = threadIdx.y; b < blocks; b += 16) s += part[(long long)b * n + i];
+    }
     red[threadIdx.y][threadIdx.x] = s;
     __syncthreads();
     if (threadIdx.y == 0 && i < n) {
         s = 0.f;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) s += red[k][threadIdx.x];
+        for (int k = 0; k < 16; ++k) s += red[k][threadIdx.x];
         out.to[i / C][i % C] = s;
     }
 }
@@ -395,68 +778,79 @@ bool make_args(const gspn_norm_desc* d, NormArgs* p) {
     return true;
 }
 
-// How a row is held: threads and vectors for each.
+// How a row is held: elements of a thread, threads of a block (128 = four warps with a row each, `warp`), up to seven places
+// kept free for the phase; `wide`: the kernels for wide rows.
 struct Shape {
-    int tpr, ch;
+    int e, threads;
+    bool warp, wide;
 };
-Shape shape_for(int C, int V) {
-    const int n = (C + V - 1) / V;
-    if (n <= 32) return {32, 1};
-    if (n <= 64) return {32, 2};
-    if (n <= 128) return {32, 4};
-    if (n <= 256) return {128, 2};
-    if (n <= 512) return {256, 2};
-    if (n <= 1024) return {512, 2};
-    if (n <= 2048) return {512, 4};
-    return {1024, 4};
+Shape shape_for(int C) {
+    const int n = C % 8 != 0 ? C + 7 : C;
+    if (n <= 256) return {8, 128, true, false};
+    if (n <= 2048) return {8, (n + 255) / 256 * 32, false, false};
+    if (n <= 4096) return {16, (n + 511) / 512 * 32, false, false};
+    return {16, (C + 511) / 512 * 32, false, true};
 }
-constexpr size_t kSumSmem = 200 * 1024;
-int bwd_blocks(const gspn_norm_desc& d) {
-    const Shape s = shape_for(d.C, d.dtype == GSPN_F32 ? 4 : 8);
-    const int rpb = s.tpr == 32 ? 4 : 1;
-    const long long groups = ((long long)d.rows + rpb - 1) / rpb;
-    const long long most = 2LL * device_sm_count() * (s.tpr <= 128 ? 2 : 1);
-    const long long n = groups < most ? groups : most;
+constexpr size_t kSmem = 200 * 1024;
+// Shared memory: parameters, or the column sums of the backward pass of wide rows.
+size_t smem_for(const Shape& s, int slots) {
+    if (s.wide) return (size_t)slots * 8 * s.threads * sizeof(f2);
+    return (size_t)s.threads * s.e * kParams * sizeof(float);
+}
+// Blocks: what fits the SMs at once by their registers (threads an SM: backward 512, 256 with 16 elements;
+// forward twice that), in whole periods of the phases, and no more than there are rows. Wide rows have
+// a block each, forward.
+int blocks_for(const gspn_norm_desc& d, bool bwd) {
+    const Shape s = shape_for(d.C);
+    const long long groups = s.warp ? ((long long)d.rows + 3) / 4 : d.rows;
+    if (s.wide && !bwd) return d.rows;
+    const int fill = (s.e == 8 ? 512 : 256) * (bwd ? 1 : 2);
+    long long n = (long long)device_sm_count() * (s.threads >= fill ? 1 : fill / s.threads);
+    n = n / 8 * 8;
+    n = groups < n ? groups : n;
     return n > 0 ? (int)n : 1;
 }
 
-template <bool FWD, typename T, typename R, int TPR, int CH>
-cudaError_t launch(const NormArgs& p, bool wide, int blocks, cudaStream_t st) {
-    constexpr int RPB = TPR == 32 ? 4 : 1, threads = TPR == 32 ? 128 : TPR;
-    if constexpr (FWD) {
-        if (wide) k_norm_fwd<T, R, TPR, CH, true><<<blocks, threads, 0, st>>>(p);
-        else k_norm_fwd<T, R, TPR, CH, false><<<blocks, threads, 0, st>>>(p);
-        return cudaSuccess;
-    } else {
-        const size_t smem = (size_t)RPB * p.slots * p.C * sizeof(float);
-        auto go = [&](auto kernel) {
-            cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-            if (e == cudaSuccess) kernel<<<blocks, threads, smem, st>>>(p);
-            return e;
-        };
-        return wide ? go(k_norm_bwd<T, R, TPR, CH, true>) : go(k_norm_bwd<T, R, TPR, CH, false>);
-    }
-}
 template <bool FWD, typename T, typename R>
-cudaError_t by_shape(const NormArgs& p, bool wide, int blocks, cudaStream_t st) {
-    const Shape s = shape_for(p.C, Vec<T>::V);
-    if (s.tpr == 32) {
-        if (s.ch == 1) return launch<FWD, T, R, 32, 1>(p, wide, blocks, st);
-        if (s.ch == 2) return launch<FWD, T, R, 32, 2>(p, wide, blocks, st);
-        return launch<FWD, T, R, 32, 4>(p, wide, blocks, st);
+cudaError_t by_shape(const NormArgs& p, int blocks, cudaStream_t st) {
+    const Shape s = shape_for(p.C);
+    const size_t smem = smem_for(s, FWD ? 0 : p.slots);
+    auto go = [&](auto kernel) {
+        cudaError_t e = cudaSuccess;
+        if (smem > 48 * 1024) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e == cudaSuccess) kernel<<<blocks, s.threads, smem, st>>>(p);
+        return e;
+    };
+    if constexpr (FWD) {
+        if (s.warp) return go(k_norm_fwd<T, R, 8, 128>);
+        if (!s.wide && s.e == 8) return go(k_norm_fwd<T, R, 8, 256>);
+        if (!s.wide) return go(k_norm_fwd<T, R, 16, 256>);
+        if (s.threads <= 512) return p.aligned ? go(k_norm_fwd_wide<T, R, 16, true, 512>) : go(k_norm_fwd_wide<T, R, 16, false, 512>);
+        return p.aligned ? go(k_norm_fwd_wide<T, R, 16, true, 1024>) : go(k_norm_fwd_wide<T, R, 16, false, 1024>);
+    } else {
+        if (s.warp) return go(k_norm_bwd<T, R, 8, 128>);
+        if (!s.wide && s.e == 8) return go(k_norm_bwd<T, R, 8, 256>);
+        if (!s.wide) return go(k_norm_bwd<T, R, 16, 256>);
+        if (s.threads <= 512) return p.aligned ? go(k_norm_bwd_wide<T, R, 16, true, 512>) : go(k_norm_bwd_wide<T, R, 16, false, 512>);
+        return p.aligned ? go(k_norm_bwd_wide<T, R, 16, true, 1024>) : go(k_norm_bwd_wide<T, R, 16, false, 1024>);
     }
-    if (s.tpr == 128) return launch<FWD, T, R, 128, 2>(p, wide, blocks, st);
-    if (s.tpr == 256) return launch<FWD, T, R, 256, 2>(p, wide, blocks, st);
-    if (s.tpr == 512 && s.ch == 2) return launch<FWD, T, R, 512, 2>(p, wide, blocks, st);
-    if (s.tpr == 512) return launch<FWD, T, R, 512, 4>(p, wide, blocks, st);
-    if constexpr (sizeof(T) == 4) return launch<FWD, T, R, 1024, 4>(p, wide, blocks, st);   // bf16 rows end at 512 x 4
-    return cudaErrorInvalidValue;
 }
 template <bool FWD>
-cudaError_t by_type(const gspn_norm_desc& d, const NormArgs& p, bool wide, int blocks, cudaStream_t st) {
-    if (d.dtype == GSPN_F32) return by_shape<FWD, float, float>(p, wide, blocks, st);
-    if (d.res_dtype == GSPN_F32) return by_shape<FWD, __nv_bfloat16, float>(p, wide, blocks, st);
-    return by_shape<FWD, __nv_bfloat16, __nv_bfloat16>(p, wide, blocks, st);
+cudaError_t by_type(const gspn_norm_desc& d, const NormArgs& p, int blocks, cudaStream_t st) {
+    if (d.dtype == GSPN_F32) return by_shape<FWD, float, float>(p, blocks, st);
+    if (d.res_dtype == GSPN_F32) return by_shape<FWD, __nv_bfloat16, float>(p, blocks, st);
+    return by_shape<FWD, __nv_bfloat16, __nv_bfloat16>(p, blocks, st);
+}
+// The least stride of the tensors' rows.
+long long least_row(const NormArgs& p, bool gate, bool r) {
+    long long s = p.C < p.y_row ? p.C : p.y_row;
+    if (gate && p.gate_row < s) s = p.gate_row;
+    if (r && p.r_row < s) s = p.r_row;
+    return s;
+}
+// True where a tensor's rows start at the phase of rows of C elements from a 16-byte border.
+bool phased(const void* p, long long row, int C, int dtype) {
+    return aligned_to(p, 16) && (row - C) % (dtype == GSPN_F32 ? 4 : 8) == 0;
 }
 
 }  // namespace
@@ -472,7 +866,7 @@ size_t gspn_norm_workspace_size(const gspn_norm_desc* desc, int for_backward) {
     NormArgs p;
     if (!make_args(desc, &p) || p.C > kMaxC) return 0;
     if (!for_backward) return 256;
-    return 256 + align256((size_t)bwd_blocks(*desc) * kSums * p.C * sizeof(float));
+    return 256 + align256((size_t)blocks_for(*desc, true) * kSums * p.C * sizeof(float));
 }
 
 gspn_status gspn_norm_forward(const gspn_norm_desc* desc, const void* y, const void* gate, const float* w_post,
@@ -493,11 +887,13 @@ gspn_status gspn_norm_forward(const gspn_norm_desc* desc, const void* y, const v
     if (p.rows == 0) return GSPN_OK;
     p.y = y; p.gate = gate; p.r = r; p.w_post = w_post; p.b_post = b_post; p.scale = scale; p.w_pre = w_pre;
     p.b_pre = b_pre; p.r_out = r_out; p.o = o;
-    bool wide = (p.C * es) % 16 == 0 && wide_ok(y, p.y_row, 0, es) && (!gate || wide_ok(gate, p.gate_row, 0, es)) &&
-                (!r || wide_ok(r, p.r_row, 0, rs)) && aligned_to(r_out, 16) && aligned_to(o, 16);
-    for (const float* q : {w_post, b_post, scale, w_pre, b_pre}) wide = wide && aligned_to(q, 16);
-    const int rpb = shape_for(p.C, desc->dtype == GSPN_F32 ? 4 : 8).tpr == 32 ? 4 : 1;
-    if (by_type<true>(*desc, p, wide, (p.rows + rpb - 1) / rpb, (cudaStream_t)stream) != cudaSuccess) return GSPN_ERR_CUDA;
+    // the phase is the storage type's: eight bf16 columns are 32 bytes of an fp32 stream
+    p.wide = phased(y, p.y_row, p.C, desc->dtype) && (!gate || phased(gate, p.gate_row, p.C, desc->dtype)) &&
+             (!r || phased(r, p.r_row, p.C, desc->dtype)) && aligned_to(r_out, 16) && aligned_to(o, 16);
+    p.least_row = least_row(p, gate != nullptr, r != nullptr);
+    p.aligned = p.wide && p.C % 8 == 0;
+    for (const float* q : {w_post, b_post, scale, w_pre, b_pre}) p.aligned = p.aligned && aligned_to(q, 16);
+    if (by_type<true>(*desc, p, blocks_for(*desc, false), (cudaStream_t)stream) != cudaSuccess) return GSPN_ERR_CUDA;
     return last_status();
 }
 
@@ -528,22 +924,23 @@ gspn_status gspn_norm_backward(const gspn_norm_desc* desc, const void* y, const 
         p.slot[i] = outs[i] ? p.slots : -1;
         if (outs[i]) to.to[p.slots++] = outs[i];
     }
-    const int rpb = shape_for(p.C, desc->dtype == GSPN_F32 ? 4 : 8).tpr == 32 ? 4 : 1;
-    // the column sums of a block live in shared memory
-    if (p.C > kMaxC || (size_t)rpb * p.slots * p.C * sizeof(float) > kSumSmem) return GSPN_ERR_UNSUPPORTED;
+    // the column sums of wide rows live in shared memory
+    if (p.C > kMaxC || smem_for(shape_for(p.C), p.slots) > kSmem) return GSPN_ERR_UNSUPPORTED;
     if (ws_bytes < gspn_norm_workspace_size(desc, 1)) return GSPN_ERR_WORKSPACE;
     p.y = y; p.gate = gate; p.r = r_out; p.w_post = w_post; p.b_post = b_post; p.scale = scale; p.w_pre = w_pre;
     p.dr = dr; p.go = go; p.dy = dy; p.dr_in = dr_in; p.dgate = dgate;
     p.part = (float*)((char*)ws + 256);
-    bool wide = (p.C * es) % 16 == 0 && wide_ok(y, p.y_row, 0, es) && (!gate || wide_ok(gate, p.gate_row, 0, es)) &&
-                (!w_pre || wide_ok(r_out, p.r_row, 0, rs)) && aligned_to(dr, 16) && aligned_to(go, 16) &&
-                aligned_to(dy, 16) && aligned_to(dr_in, 16) && aligned_to(dgate, 16);
-    for (const float* q : {w_post, b_post, scale, w_pre}) wide = wide && aligned_to(q, 16);
-    const int blocks = bwd_blocks(*desc);
+    p.wide = phased(y, p.y_row, p.C, desc->dtype) && (!gate || phased(gate, p.gate_row, p.C, desc->dtype)) &&
+             (!w_pre || phased(r_out, p.r_row, p.C, desc->dtype)) && aligned_to(dr, 16) && aligned_to(go, 16) &&
+             aligned_to(dy, 16) && aligned_to(dr_in, 16) && aligned_to(dgate, 16);
+    p.least_row = least_row(p, gate != nullptr, w_pre != nullptr);
+    p.aligned = p.wide && p.C % 8 == 0;
+    for (const float* q : {w_post, b_post, scale, w_pre}) p.aligned = p.aligned && aligned_to(q, 16);
+    const int blocks = blocks_for(*desc, true);
     cudaStream_t st = (cudaStream_t)stream;
-    if (by_type<false>(*desc, p, wide, blocks, st) != cudaSuccess) return GSPN_ERR_CUDA;
+    if (by_type<false>(*desc, p, blocks, st) != cudaSuccess) return GSPN_ERR_CUDA;
     const int n = p.slots * p.C;
-    if (n > 0) k_norm_sum<<<(n + 31) / 32, dim3(32, 8), 0, st>>>(p.part, blocks, n, p.C, to);
+    if (n > 0) k_norm_sum<<<(n + 31) / 32, dim3(32, 16), 0, st>>>(p.part, blocks, n, p.C, to);
     return last_status();
 }
 
