@@ -11,6 +11,8 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libgspn.so")
+BINDING_SRC = os.path.join(CSRC, "seq_binding.cpp")
+BINDING = os.path.join(HERE, "_seq_fast.so")
 
 NVCC_FLAGS = [
     "-O3", "-std=c++17", "-gencode", "arch=compute_100a,code=sm_100a", "-lineinfo",
@@ -28,10 +30,26 @@ def headers():
 
 
 def stale() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(BINDING):
         return True
-    t = os.path.getmtime(LIB)
-    return any(os.path.getmtime(f) > t for f in sources() + headers() + [__file__])
+    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
+    return any(os.path.getmtime(f) > t for f in sources() + headers() + [BINDING_SRC, __file__])
+
+
+def binding_command(out: str):
+    """g++ for the binding of the token-sequence calls: a CPython module against torch's headers, which
+    calls libgspn's entry points by address."""
+    import sysconfig
+
+    import torch
+
+    troot = os.path.dirname(torch.__file__)
+    inc = [os.path.join(troot, "include"), os.path.join(troot, "include", "torch", "csrc", "api", "include"),
+           os.path.join(os.environ.get("CUDA_HOME", "/usr/local/cuda"), "include"), sysconfig.get_paths()["include"]]
+    lib = os.path.join(troot, "lib")
+    return [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *[f for p in inc for f in ("-isystem", p)],
+            "-I", INCLUDE, BINDING_SRC, "-o", out, "-L", lib, "-ltorch_python", "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda"]
 
 
 def build(force: bool = False, verbose: bool = False, extra=()) -> str:
@@ -49,12 +67,15 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
             print(" ".join(cmd), file=sys.stderr)
         procs.append((subprocess.Popen(cmd), src))
         objs.append(obj)
+    tmp_binding = BINDING + f".tmp{os.getpid()}"
+    procs.append((subprocess.Popen(binding_command(tmp_binding)), BINDING_SRC))
     for p, src in procs:
         if p.wait() != 0:
-            raise RuntimeError(f"nvcc failed on {src}")
+            raise RuntimeError(f"the compiler failed on {src}")
     tmp = LIB + f".tmp{os.getpid()}"
     subprocess.check_call([nvcc, "-shared", "-gencode", "arch=compute_100a,code=sm_100a", "-o", tmp, *objs])
     os.replace(tmp, LIB)
+    os.replace(tmp_binding, BINDING)
     return LIB
 
 

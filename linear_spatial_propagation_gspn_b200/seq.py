@@ -71,6 +71,35 @@ def _ok(status, what):
         raise _pkg().GspnError(status, what)
 
 
+def _decline(*args):
+    return None
+
+
+class _Fast:
+    """The calls of csrc/seq_binding.cpp: each makes the whole call, or returns None for the checks here to
+    say why not. Looked up once, when the library is first needed; without the module (a tree that was
+    built before it) every call goes through the checks here."""
+
+    def __getattr__(self, name):
+        fns = dict.fromkeys(("conv_forward", "conv_backward", "conv_step", "ssm_forward", "ssm_backward", "ssm_step", "norm_forward",
+                             "norm_backward"), _decline)
+        if name not in fns:
+            raise AttributeError(name)
+        L = _pkg().lib()
+        try:
+            from . import _seq_fast
+
+            _seq_fast.init({n: ctypes.cast(getattr(L, n), ctypes.c_void_p).value for n in SIGNATURES})
+            fns = {n: getattr(_seq_fast, n) for n in fns}
+        except ImportError:
+            pass
+        self.__dict__.update(fns)
+        return fns[name]
+
+
+_fast = _Fast()
+
+
 # Descriptors by their values: building one costs more than a small call's launch.
 @functools.lru_cache(maxsize=1024)
 def _desc(kind, *values):
@@ -202,11 +231,19 @@ def _conv_args(x, w, bias, silu, cu):
     return values, (n, K - 1, C)
 
 
-@_on_device
-def conv_forward(x, w, bias=None, silu=True, cu=None, state0=None, y=None, state=None):
+def conv_forward(x, w, bias=None, silu=True, cu=None, state0=None, y=None, state=None, stream=None):
     """y_t = act(bias + sum_k w[:, k] x_{t-K+1+k}), act = silu or nothing. x: (B, L, C); w: (C, K), K = 2..4;
     state0: (S or B, K-1, C), what lies before each sequence, oldest first (default zeros); state, of
     the same shape, receives the last K-1 inputs of each and may be state0."""
+    if stream is None:
+        done = _fast.conv_forward(x, w, bias, cu, state0, y, state, silu)
+        if done is not None:
+            return done
+    return _conv_forward(x, w, bias, silu, cu, state0, y, state, stream=stream)
+
+
+@_on_device
+def _conv_forward(x, w, bias, silu, cu, state0, y, state):
     values, ss = _conv_args(x, w, bias, silu, cu)
     dev, dt = x.device, x.dtype
     _opt("state0", state0, ss, dt, dev)
@@ -217,10 +254,18 @@ def conv_forward(x, w, bias=None, silu=True, cu=None, state0=None, y=None, state
     return y
 
 
-@_on_device
-def conv_backward(x, w, bias, dy, silu=True, cu=None, state0=None, dstate=None, out=None):
+def conv_backward(x, w, bias, dy, silu=True, cu=None, state0=None, dstate=None, out=None, stream=None):
     """Gradients (dx, dw, dbias, dstate0) of sum(dy y) + sum(dstate state); None for what was not given.
     out: tensors to write them to, in that order."""
+    if stream is None and out is None:
+        done = _fast.conv_backward(x, w, bias, cu, state0, dy, dstate, silu)
+        if done is not None:
+            return done
+    return _conv_backward(x, w, bias, dy, silu, cu, state0, dstate, out, stream=stream)
+
+
+@_on_device
+def _conv_backward(x, w, bias, dy, silu, cu, state0, dstate, out):
     values, ss = _conv_args(x, w, bias, silu, cu)
     dev, dt = x.device, x.dtype
     _is("dy", dy, x.shape, dt, dev)
@@ -241,11 +286,19 @@ def conv_backward(x, w, bias, dy, silu=True, cu=None, state0=None, dstate=None, 
     return dx, dw, db, ds
 
 
-@_on_device
-def conv_step(x, w, bias, state, idx=None, silu=True, y=None):
+def conv_step(x, w, bias, state, idx=None, silu=True, y=None, stream=None):
     """One token for each row. x: (B, C); state: (slots, K-1, C), moved on in place; idx: (B,) int32, each
     row's slot (default: its number). A row whose index is no slot is skipped; rows that name the
     same slot take their tokens in row order."""
+    if stream is None:
+        done = _fast.conv_step(x, w, bias, state, idx, y, silu)
+        if done is not None:
+            return done
+    return _conv_step(x, w, bias, state, idx, silu, y, stream=stream)
+
+
+@_on_device
+def _conv_step(x, w, bias, state, idx, silu, y):
     if x.dim() != 2:
         raise ValueError("x must be (B, C)")
     if w.dim() != 2:
@@ -284,7 +337,7 @@ def _ssm_args(x, dt, A, Bm, Cm, D, z, dt_bias, softplus, cu):
     return (B, L, C, G, N, S, _code(ty), int(bool(softplus)), *strides), (n, C, N)
 
 
-def _ssm_forward(x, dt, A, Bm, Cm, D, z, dt_bias, softplus, cu, h0, y, h, save):
+def _ssm_run(x, dt, A, Bm, Cm, D, z, dt_bias, softplus, cu, h0, y, h, save):
     values, ss = _ssm_args(x, dt, A, Bm, Cm, D, z, dt_bias, softplus, cu)
     dev = x.device
     _opt("h0", h0, ss, torch.float32, dev)
@@ -300,25 +353,52 @@ def _ssm_forward(x, dt, A, Bm, Cm, D, z, dt_bias, softplus, cu, h0, y, h, save):
     return y, hsave
 
 
-@_on_device
-def ssm_forward(x, dt, A, Bm, Cm, D=None, z=None, dt_bias=None, softplus=True, cu=None, h0=None, y=None, h=None):
+def ssm_forward(x, dt, A, Bm, Cm, D=None, z=None, dt_bias=None, softplus=True, cu=None, h0=None, y=None, h=None,
+                stream=None):
     """h_t = exp(d_t A) h_{t-1} + d_t x_t B_t, y_t = (C_t h_t + D x_t) silu(z_t), with d = dt + dt_bias taken
     through softplus unless softplus is false. x, dt, z: (B, L, C); Bm, Cm: (B, L, G, N), G dividing C;
     A: (C, N), N <= 64; D, dt_bias: (C,). h0: (S or B, C, N) fp32, the states before the sequences
     (default zeros); h, of the same shape, receives the ones behind them and may be h0."""
-    return _ssm_forward(x, dt, A, Bm, Cm, D, z, dt_bias, softplus, cu, h0, y, h, False)[0]
+    if stream is None:
+        done = _fast.ssm_forward(x, dt, A, Bm, Cm, D, z, dt_bias, cu, h0, y, h, softplus, False)
+        if done is not None:
+            return done
+    return _ssm_forward(x, dt, A, Bm, Cm, D, z, dt_bias, softplus, cu, h0, y, h, stream=stream)
 
 
 @_on_device
-def ssm_forward_save(x, dt, A, Bm, Cm, D=None, z=None, dt_bias=None, softplus=True, cu=None, h0=None, y=None, h=None):
+def _ssm_forward(x, dt, A, Bm, Cm, D, z, dt_bias, softplus, cu, h0, y, h):
+    return _ssm_run(x, dt, A, Bm, Cm, D, z, dt_bias, softplus, cu, h0, y, h, False)[0]
+
+
+def ssm_forward_save(x, dt, A, Bm, Cm, D=None, z=None, dt_bias=None, softplus=True, cu=None, h0=None, y=None, h=None,
+                     stream=None):
     """Training forward: y as ssm_forward, and the states (a flat fp32 tensor) that ssm_backward starts from."""
-    return _ssm_forward(x, dt, A, Bm, Cm, D, z, dt_bias, softplus, cu, h0, y, h, True)
+    if stream is None:
+        done = _fast.ssm_forward(x, dt, A, Bm, Cm, D, z, dt_bias, cu, h0, y, h, softplus, True)
+        if done is not None:
+            return done
+    return _ssm_forward_save(x, dt, A, Bm, Cm, D, z, dt_bias, softplus, cu, h0, y, h, stream=stream)
 
 
 @_on_device
-def ssm_backward(x, dt, A, Bm, Cm, dy, hsave, D=None, z=None, dt_bias=None, softplus=True, cu=None, h0=None, dh=None, out=None):
+def _ssm_forward_save(x, dt, A, Bm, Cm, D, z, dt_bias, softplus, cu, h0, y, h):
+    return _ssm_run(x, dt, A, Bm, Cm, D, z, dt_bias, softplus, cu, h0, y, h, True)
+
+
+def ssm_backward(x, dt, A, Bm, Cm, dy, hsave, D=None, z=None, dt_bias=None, softplus=True, cu=None, h0=None, dh=None, out=None,
+                 stream=None):
     """Gradients (dx, ddt, dA, dBm, dCm, dD, dz, ddt_bias, dh0) of sum(dy y) + sum(dh h), None for what was not
     given; hsave from ssm_forward_save on the same inputs. out: tensors to write them to, in that order."""
+    if stream is None and out is None:
+        done = _fast.ssm_backward(x, dt, A, Bm, Cm, dy, hsave, D, z, dt_bias, cu, h0, dh, softplus)
+        if done is not None:
+            return done
+    return _ssm_backward(x, dt, A, Bm, Cm, dy, hsave, D, z, dt_bias, softplus, cu, h0, dh, out, stream=stream)
+
+
+@_on_device
+def _ssm_backward(x, dt, A, Bm, Cm, dy, hsave, D, z, dt_bias, softplus, cu, h0, dh, out):
     values, ss = _ssm_args(x, dt, A, Bm, Cm, D, z, dt_bias, softplus, cu)
     dev, ty, f = x.device, x.dtype, torch.float32
     _is("dy", dy, x.shape, ty, dev)
@@ -348,10 +428,18 @@ def ssm_backward(x, dt, A, Bm, Cm, dy, hsave, D=None, z=None, dt_bias=None, soft
     return dx, ddt, dA, dB, dC, dD, dz, dbias, dh0
 
 
-@_on_device
-def ssm_step(x, dt, A, Bm, Cm, h, D=None, z=None, dt_bias=None, softplus=True, idx=None, y=None):
+def ssm_step(x, dt, A, Bm, Cm, h, D=None, z=None, dt_bias=None, softplus=True, idx=None, y=None, stream=None):
     """One token for each row. x, dt, z: (B, C); Bm, Cm: (B, G, N); h: (slots, C, N) fp32, moved on in place;
     idx as for conv_step."""
+    if stream is None:
+        done = _fast.ssm_step(x, dt, A, Bm, Cm, h, D, z, dt_bias, idx, y, softplus)
+        if done is not None:
+            return done
+    return _ssm_step(x, dt, A, Bm, Cm, h, D, z, dt_bias, softplus, idx, y, stream=stream)
+
+
+@_on_device
+def _ssm_step(x, dt, A, Bm, Cm, h, D, z, dt_bias, softplus, idx, y):
     if x.dim() != 2 or Bm.dim() != 3:
         raise ValueError("x must be (B, C), Bm and Cm (B, G, N)")
     (B, C), (G, N) = x.shape, Bm.shape[1:]
@@ -421,13 +509,21 @@ def _norm_args(y, gate, w_post, b_post, scale, r, w_pre, b_pre, eps, center, res
             0 if r is None else _rows("r", r, y.shape, (y.dtype, torch.float32), dev))
 
 
-@_on_device
 def norm_forward(y, r=None, gate=None, w_post=None, b_post=None, scale=None, w_pre=None, b_pre=None, eps=1e-5, center=False,
-                 r_out=None, o=None):
+                 r_out=None, o=None, stream=None):
     """(r_out, o): r_out = r + scale * (norm(y silu(gate)) w_post + b_post) and o = norm(r_out) w_pre + b_pre, the end
     of one block and the beginning of the next in one pass. norm(v) = v / sqrt(mean(v^2) + eps), of
     v - mean(v) if center. y, gate: (..., C); r of y's dtype or fp32, and r_out with it. Whatever is None
     is left out (no w_post or w_pre: no norm there; no w_pre: o is None; no r: r_out has y's dtype)."""
+    if stream is None:
+        done = _fast.norm_forward(y, r, gate, w_post, b_post, scale, w_pre, b_pre, r_out, o, eps, center)
+        if done is not None:
+            return done
+    return _norm_forward(y, r, gate, w_post, b_post, scale, w_pre, b_pre, eps, center, r_out, o, stream=stream)
+
+
+@_on_device
+def _norm_forward(y, r, gate, w_post, b_post, scale, w_pre, b_pre, eps, center, r_out, o):
     rt = y.dtype if r is None else r.dtype
     values = _norm_args(y, gate, w_post, b_post, scale, r, w_pre, b_pre, eps, center, rt)
     dev = y.device
@@ -441,12 +537,20 @@ def norm_forward(y, r=None, gate=None, w_post=None, b_post=None, scale=None, w_p
     return r_out, o
 
 
-@_on_device
 def norm_backward(y, r_out, dr, do, gate=None, w_post=None, b_post=None, scale=None, w_pre=None, b_pre=None, eps=1e-5,
-                  center=False):
+                  center=False, stream=None):
     """Gradients (dy, dr_in, dgate, dw_post, db_post, dscale, dw_pre, db_pre) of sum(dr r_out) + sum(do o), None for what
     was not given. r_out is norm_forward's; dr_in is the gradient of its r (of r_out's dtype). dr may be
     None (the stream behind the block is not used); do goes with w_pre, and without it r_out may be None."""
+    if stream is None:
+        done = _fast.norm_backward(y, r_out, dr, do, gate, w_post, b_post, scale, w_pre, b_pre, eps, center)
+        if done is not None:
+            return done
+    return _norm_backward(y, r_out, dr, do, gate, w_post, b_post, scale, w_pre, b_pre, eps, center, stream=stream)
+
+
+@_on_device
+def _norm_backward(y, r_out, dr, do, gate, w_post, b_post, scale, w_pre, b_pre, eps, center):
     if (w_pre is None) != (do is None):
         raise ValueError("do goes with w_pre")
     if r_out is None and dr is None or r_out is None and w_pre is not None:
