@@ -2,7 +2,7 @@
 //   u_t = bias + sum_{k<K} w_k x_{t-K+1+k},   y_t = u_t or u_t sigmoid(u_t).
 //
 // A few operations per element, so memory traffic bounds it: x read and y written once. A thread
-// keeps a vector of channels (16 bytes forward) and walks a run of tokens with the K - 1 inputs
+// keeps four channels (eight of bf16 took registers that more warps use better) and walks a run of tokens with the K - 1 inputs
 // before the present one in registers, so each input is loaded once per run; the K - 1 tokens that
 // neighbouring runs share come from the caches.
 #include "seq_common.cuh"
@@ -14,6 +14,7 @@ namespace {
 constexpr int kRunFwd = 16;     // tokens of a thread, forward
 constexpr int kRunBwd = 32;     // tokens of a thread, backward
 constexpr int kBatch = 4;       // tokens whose loads are in flight together
+constexpr int kVB = 4;          // channels of a thread
 
 struct ConvArgs {
     int B, L, C, S, silu;
@@ -131,7 +132,7 @@ template <typename T, int K> __device__ void last_inputs(const ConvArgs& p, long
 // Blocks behind the first `tokens` take the states behind the sequences.
 template <typename T, int K>
 __global__ void __launch_bounds__(128) k_conv_fwd(const ConvArgs p, long long blocks) {
-    constexpr int V = Vec<T>::V, P = V / 2;
+    constexpr int P = kVB / 2;
     if (blockIdx.x >= blocks) {
         last_inputs<T, K>(p, (blockIdx.x - blocks) * (long long)blockDim.x + threadIdx.x);
         return;
@@ -143,23 +144,23 @@ __global__ void __launch_bounds__(128) k_conv_fwd(const ConvArgs p, long long bl
     if (row >= p.B) return;
     int t = (int)(rr % p.runs) * p.run;
     const int te = min(t + p.run, p.L);
-    const int c = cv * V, n = p.C - c;
+    const int c = cv * kVB, n = p.C - c;
     if (p.cu) t = max(t, cu_at(p, 0));
     if (t >= te) return;
     const T* xr = (const T*)p.x + row * p.x_row + c;
     T* yr = (T*)p.y + (long long)row * p.L * p.C + c;
-    uint4 raw[kBatch], next[kBatch];
+    typedef typename Raw<T, P>::type R;
+    R raw[kBatch], next[kBatch];
     auto load = [&](int t) {
 #pragma unroll
-        for (int u = 0; u < kBatch; ++u)
-            next[u] = t + u < te ? ld_raw<T>(xr + (t + u) * p.x_tok, n, p.wide) : make_uint4(0, 0, 0, 0);
+        for (int u = 0; u < kBatch; ++u) next[u] = t + u < te ? ld_pairs_raw<T, P>(xr + (t + u) * p.x_tok, n, p.wide) : R{};
     };
     load(t);
     f2 w[K][P], b[P], win[K][P];
     load_taps<K, P>(p, c, n, w, b);
     Seq s = find(p, row, t);
     window<T, K, P>(p, xr, s, t, c, n, win);
-    auto one = [&](const uint4& q, int t) {
+    auto one = [&](const R& q, int t) {
         to_pairs(q, win[K - 1]);
         f2 o[P];
 #pragma unroll
@@ -227,7 +228,7 @@ __global__ void k_conv_state(const ConvArgs p) {
 // adds to in registers: after token t the one of t - K + 1 is complete. It goes K - 1 tokens past
 // its run for its last sums. A block is 32 channel vectors (4 channels) x 4 runs; it takes several
 // runs in turn and keeps its sums of dw and dbias until the end; k_conv_sum adds the blocks in order.
-constexpr int kVB = 4, kRows = 4;
+constexpr int kRows = 4;
 
 template <typename T, int K>
 __global__ void __launch_bounds__(128) k_conv_bwd(const ConvArgs p) {
@@ -454,42 +455,46 @@ __global__ void k_conv_dstate(const ConvArgs p) {
 }
 
 // ----------------------------------------------------------------------------------- one token
-// Thread = a vector of channels of one row. Rows that name the slot of an earlier row leave their
-// token to that row, which takes them in order.
+// Thread = four channels of the block's `group` rows, one after the other, with their filters read once
+// and the next row's state fetched ahead. Rows that name the slot of an earlier row leave their token to
+// that row, which takes them in order.
+constexpr int kGroup = 8;
+
 template <typename T, int K>
-__global__ void __launch_bounds__(128) k_conv_step(const ConvArgs p, const int* idx, int slots) {
-    constexpr int V = Vec<T>::V;
-    const int b0 = blockIdx.y;
-    const int slot = idx ? idx[b0] : b0;
-    if (slot < 0 || slot >= slots) return;
-    int more = 0;
-    if (idx) {
-        bool earlier = false, later = false;
-        for (int b = threadIdx.x; b < p.B; b += blockDim.x) {
-            const bool same = b != b0 && idx[b] == slot;
-            earlier |= same && b < b0;
-            later |= same && b > b0;
-        }
-        if (__syncthreads_or(earlier)) return;
-        more = __syncthreads_or(later);
-    }
-    constexpr int P = V / 2;
-    const int c = (blockIdx.x * blockDim.x + threadIdx.x) * V, n = p.C - c;
-    if (n <= 0) return;
-    T* st = (T*)p.state + (long long)slot * (K - 1) * p.C + c;
-    uint4 win[K];
+__global__ void __launch_bounds__(128) k_conv_step(const ConvArgs p, const int* idx, int slots, int group) {
+    constexpr int P = kVB / 2;
+    typedef typename Raw<T, P>::type R;
+    __shared__ unsigned flags[2];                                 // rows of the group with an earlier, a later row of their slot
+    const int b0 = blockIdx.y * group, rows = min(group, p.B - b0);
+    const int c = (blockIdx.x * blockDim.x + threadIdx.x) * kVB, n = p.C - c;   // n <= 0: no channels, for the barriers only
+    auto slot_of = [&](int r) { return r < rows ? (idx ? idx[b0 + r] : b0 + r) : -1; };
+    R win[K], next[K];
+    auto fetch = [&](int r, int slot) {
+        if (slot < 0 || slot >= slots || n <= 0) return;
+        const T* st = (const T*)p.state + (long long)slot * (K - 1) * p.C + c;
+#pragma unroll
+        for (int j = 0; j < K - 1; ++j) next[j] = ld_pairs_raw<T, P>(st + (long long)j * p.C, n, p.wide);
+        next[K - 1] = ld_pairs_raw<T, P>((const T*)p.x + (b0 + r) * p.x_row + c, n, p.wide);
+    };
+    int slot = slot_of(0);
+    fetch(0, slot);
     f2 w[K][P], bias[P];
-#pragma unroll
-    for (int j = 0; j < K - 1; ++j) win[j] = ld_raw<T>(st + (long long)j * p.C, n, p.wide);
-    win[K - 1] = ld_raw<T>((const T*)p.x + b0 * p.x_row + c, n, p.wide);
-    load_taps<K, P>(p, c, n, w, bias);
-    for (int b = b0; b < (more ? p.B : b0 + 1); ++b) {
-        if (b != b0) {
-            if (idx[b] != slot) continue;
-#pragma unroll
-            for (int k = 0; k < K - 1; ++k) win[k] = win[k + 1];
-            win[K - 1] = ld_raw<T>((const T*)p.x + b * p.x_row + c, n, p.wide);
+    if (n > 0) load_taps<K, P>(p, c, n, w, bias);
+    unsigned earlier = 0, later = 0;
+    if (idx) {
+        if (threadIdx.x < 2) flags[threadIdx.x] = 0;
+        __syncthreads();
+        for (int b = threadIdx.x; b < p.B; b += blockDim.x) {
+            const int s = idx[b];
+            for (int r = 0; r < rows; ++r)
+                if (b != b0 + r && s == idx[b0 + r]) atomicOr(&flags[b > b0 + r], 1u << r);
         }
+        __syncthreads();
+        earlier = flags[0];
+        later = flags[1];
+    }
+    if (n <= 0) return;
+    auto token = [&](int b) {
         f2 o[P];
 #pragma unroll
         for (int i = 0; i < P; ++i) o[i] = bias[i];
@@ -505,16 +510,34 @@ __global__ void __launch_bounds__(128) k_conv_step(const ConvArgs p, const int* 
             for (int i = 0; i < P; ++i) o[i] = silu2(o[i]);
         }
         st_pairs<T, P>((T*)p.y + (long long)b * p.C + c, o, n, p.wide);
-    }
+    };
+    for (int r = 0; r < rows; ++r) {
+        const int now = slot;
 #pragma unroll
-    for (int j = 0; j < K - 1; ++j) {
-        T* to = st + (long long)j * p.C;
-        if (p.wide && n >= V) {
-            *(uint4*)to = win[j + 1];
-        } else {
-            float f[V];
-            unpack_raw<T>(win[j + 1], f);
-            st_vec<T>(to, f, n, false);
+        for (int k = 0; k < K; ++k) win[k] = next[k];
+        slot = slot_of(r + 1);
+        fetch(r + 1, slot);                                       // of no use to a row that leaves its token to another
+        if (now < 0 || now >= slots || (earlier >> r & 1)) continue;
+        token(b0 + r);
+        if (later >> r & 1) {
+            for (int b = b0 + r + 1; b < p.B; ++b) {
+                if (idx[b] != now) continue;
+#pragma unroll
+                for (int k = 0; k < K - 1; ++k) win[k] = win[k + 1];
+                win[K - 1] = ld_pairs_raw<T, P>((const T*)p.x + b * p.x_row + c, n, p.wide);
+                token(b);
+            }
+        }
+        T* st = (T*)p.state + (long long)now * (K - 1) * p.C + c;
+#pragma unroll
+        for (int j = 0; j < K - 1; ++j) {
+            if (p.wide && n >= kVB) {
+                *(R*)(st + (long long)j * p.C) = win[j + 1];
+            } else {
+                float f[kVB];
+                unpack_quad(win[j + 1], f);
+                st_quad<T>(st + (long long)j * p.C, f, n, false);
+            }
         }
     }
 }
@@ -589,8 +612,7 @@ gspn_status gspn_conv_forward(const gspn_conv_desc* desc, const void* x, const f
     p.x = x; p.w = w; p.bias = bias; p.cu = cu; p.state0 = state0; p.y = y; p.state = state;
     p.wide = (p.C * es) % 16 == 0 && wide_ok(x, p.x_row, p.x_tok, es) && aligned_to(y, 16) && aligned_to(state0, 16);
     p.wide_w = aligned_to(w, 16);
-    const int V = desc->dtype == GSPN_F32 ? 4 : 8;
-    p.nvec = (p.C + V - 1) / V;
+    p.nvec = (p.C + kVB - 1) / kVB;
     // Short inputs are cut into runs of kBatch tokens, so that more threads share them.
     const long long threads16 = (long long)p.B * ((p.L + kRunFwd - 1) / kRunFwd) * p.nvec;
     p.run = threads16 >= 1024LL * device_sm_count() ? kRunFwd : kBatch;
@@ -663,13 +685,16 @@ gspn_status gspn_conv_step(const gspn_conv_desc* desc, const void* x, const floa
     p.x = x; p.w = w; p.bias = bias; p.y = y; p.state = state;
     p.wide = (p.C * es) % 16 == 0 && wide_ok(x, p.x_row, 0, es) && aligned_to(y, 16) && aligned_to(state, 16);
     p.wide_w = aligned_to(w, 16);
-    const int V = desc->dtype == GSPN_F32 ? 4 : 8;
-    const int nvec = (p.C + V - 1) / V;
+    // rows share a block (and its filters) as far as four blocks remain for each SM
+    const long long gx = (p.C + 128 * kVB - 1) / (128 * kVB);
+    long long group = gx * p.B / (4LL * device_sm_count());
+    group = group < 1 ? 1 : group > kGroup ? kGroup : group;
+    const dim3 grid((unsigned)gx, (unsigned)((p.B + group - 1) / group));
     cudaStream_t st = (cudaStream_t)stream;
     with_taps(desc->dtype, desc->K, [&](auto t, auto k) {
         using T = decltype(t);
         constexpr int K = decltype(k)::value;
-        k_conv_step<T, K><<<dim3((nvec + 127) / 128, p.B), 128, 0, st>>>(p, idx, slots);
+        k_conv_step<T, K><<<grid, 128, 0, st>>>(p, idx, slots, (int)group);
     });
     return last_status();
 }

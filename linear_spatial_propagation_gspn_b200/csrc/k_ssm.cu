@@ -34,7 +34,7 @@ struct SsmArgs {
     int K;                   // pieces of a sequence
     int nb, nbb;             // channel blocks of a group; of a backward block's size
     int softplus;
-    bool wide;               // x, dt, z, y (and dy and the gradients) have 16-byte aligned vectors
+    bool wide, wide_bc;      // x, dt, z, y (and dy and the gradients) have 16-byte aligned vectors; B and C have (a step's)
     const void *x, *dt, *z, *Bm, *Cm;
     long long x_row, x_tok, dt_row, dt_tok, z_row, z_tok, b_row, b_tok, c_row, c_tok;
     const float *A, *D, *bias, *h0;
@@ -976,75 +976,171 @@ __global__ void k_ssm_sum_ac(const float* dA_part, const float* dch_part, int sl
 }
 
 // ----------------------------------------------------------------------------------- one token
-// A block takes one row and as many channels as its threads hold four states of. Rows that name the
-// slot of an earlier row leave their token to that row, which walks them in order.
-template <typename T>
-__global__ void k_ssm_step(const SsmArgs p, const int* idx, int slots, int NL) {
-    const int b0 = blockIdx.y;
-    const int slot = idx ? idx[b0] : b0;
-    if (slot < 0 || slot >= slots) return;
-    int more = 0;
-    if (idx) {
-        bool earlier = false, later = false;
-        for (int b = threadIdx.x; b < p.B; b += blockDim.x) {
-            const bool same = b != b0 && idx[b] == slot;
-            earlier |= same && b < b0;
-            later |= same && b > b0;
-        }
-        if (__syncthreads_or(earlier)) return;
-        more = __syncthreads_or(later);
-    }
-    const int nl = threadIdx.x % NL, n0 = 4 * nl;
-    const long long c = (long long)blockIdx.x * (blockDim.x / NL) + threadIdx.x / NL;
-    const bool cok = c < p.C;
-    const int g = cok ? (int)(c / (p.C / p.G)) : 0;
-    float h[4], A2[4];
-    float* hp = p.h + ((long long)slot * p.C + c) * p.N + n0;
-    const bool vec = (p.N & 3) == 0 && p.wide;
-    if (vec && cok && n0 < p.N) {
-        const float4 f = *(const float4*)hp, a = *(const float4*)(p.A + c * p.N + n0);
-        h[0] = f.x; h[1] = f.y; h[2] = f.z; h[3] = f.w;
-        A2[0] = a.x * kLog2e; A2[1] = a.y * kLog2e; A2[2] = a.z * kLog2e; A2[3] = a.w * kLog2e;
-    } else {
+// State traffic bounds it: 8 N bytes a row and channel. A lane holds four states of I channels. I = 4 (as
+// far apart as the block is wide) puts four 16-byte loads of the state in flight, and each of a
+// channel's lanes does the scalar work of one of the four channels (step size, gate, output) and hands
+// the step to the others; I = 1 has more blocks for few rows. A, which is as large as a row's state, is
+// read once for the block's `group` rows, and the next row's state is fetched ahead. Rows that name the
+// slot of an earlier row leave their token to that row, which takes them in order.
+constexpr int kStep = 128, kGroup = 8;
+
+// PLAIN: full blocks of one group whose states fill their lanes with aligned vectors (N = 4 NL, C a multiple
+// of the block's channels): without the general form's checks and 64-bit offsets, which were most of
+// its instructions (256 rows of 4096 channels: 620 for each warp and row).
+template <typename T, int NL, int I, bool PLAIN>
+__global__ void __launch_bounds__(kStep) k_ssm_step(const SsmArgs p, const int* idx, int slots, int group) {
+    constexpr unsigned all = 0xffffffffu;
+    constexpr int CH = kStep / NL;                                // distance of a lane's channels
+    __shared__ unsigned flags[2];                                 // rows of the group with an earlier, a later row of their slot
+    const int b0 = blockIdx.y * group, rows = min(group, p.B - b0);
+    const int lane = threadIdx.x & 31, nl = threadIdx.x % NL, n0 = 4 * nl, base = lane - nl;
+    const long long c0 = (long long)blockIdx.x * I * CH + threadIdx.x / NL;
+    const long long cm = c0 + (nl & (I - 1)) * CH;                // the channel of this lane's scalar work
+    const bool mine = PLAIN || cm < p.C;
+    const int Cg = p.C / p.G;
+    const bool vec = PLAIN || p.wide;                             // N a multiple of four, h and A aligned
+    const bool same_group = PLAIN || p.G == 1;
+
+    // Offsets of the lane's states in a row's state (C N < 2^30).
+    const unsigned N = PLAIN ? 4u * NL : (unsigned)p.N, at0 = (unsigned)c0 * N + n0, at_step = CH * N;
+    bool in[I];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const bool ok = cok && n0 + j < p.N;
-            h[j] = ok ? hp[j] : 0.f;
-            A2[j] = ok ? p.A[c * p.N + n0 + j] * kLog2e : 0.f;
+    for (int i = 0; i < I; ++i) in[i] = PLAIN || c0 + i * CH < p.C;
+    auto read4 = [&](const float* s, f2 (&v)[2]) {                // four states of a channel
+        v[0] = v[1] = both(0.f);
+        if (vec) {
+            if (PLAIN || n0 < p.N) ld_pairs(s, v[0], v[1]);
+        } else {
+            float f[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (n0 + j < p.N) f[j] = s[j];
+            v[0] = pack(f[0], f[1]);
+            v[1] = pack(f[2], f[3]);
         }
+    };
+    auto slot_of = [&](int r) { return r < rows ? (idx ? idx[b0 + r] : b0 + r) : -1; };
+    f2 h[I][2], next[I][2];
+    auto fetch = [&](int slot) {
+        if (slot < 0 || slot >= slots) return;
+        const float* hp = p.h + (long long)slot * p.C * p.N;
+#pragma unroll
+        for (int i = 0; i < I; ++i)
+            if (in[i]) read4(hp + (at0 + i * at_step), next[i]);
+    };
+    int slot = slot_of(0);
+    fetch(slot);
+    f2 A2[I][2];
+    int g[I];
+#pragma unroll
+    for (int i = 0; i < I; ++i) {
+        A2[i][0] = A2[i][1] = both(0.f);
+        if (in[i]) read4(p.A + (at0 + i * at_step), A2[i]);
+        A2[i][0] = mul2(A2[i][0], both(kLog2e));
+        A2[i][1] = mul2(A2[i][1], both(kLog2e));
+        g[i] = in[i] && !same_group ? (int)((c0 + i * CH) / Cg) : 0;
     }
-    for (int b = b0; b < (more ? p.B : b0 + 1); ++b) {
-        if (b != b0 && idx[b] != slot) continue;
+    const float D = mine && p.D ? p.D[cm] : 0.f, bias = mine && p.bias ? p.bias[cm] : 0.f;
+
+    auto token = [&](int b) {
         float x = 0.f, d = 0.f, z = 0.f;
-        if (cok) {
-            x = Io<T>::ld((const T*)p.x + b * p.x_row + c);
-            d = Io<T>::ld((const T*)p.dt + b * p.dt_row + c) + (p.bias ? p.bias[c] : 0.f);
-            if (p.z) z = Io<T>::ld((const T*)p.z + b * p.z_row + c);
+        if (mine) {
+            x = Io<T>::ld((const T*)p.x + b * p.x_row + cm);
+            d = Io<T>::ld((const T*)p.dt + b * p.dt_row + cm) + bias;
+            if (p.z) z = Io<T>::ld((const T*)p.z + b * p.z_row + cm);
         }
+        f2 bv[2], cv[2];
+        auto states = [&](int gi) {
+            const T* bp = (const T*)p.Bm + b * p.b_row + (long long)gi * p.N + n0;
+            const T* cp = (const T*)p.Cm + b * p.c_row + (long long)gi * p.N + n0;
+            float f[4];
+            unpack_quad(ld_quad(bp, PLAIN ? 4 : p.N - n0, PLAIN || p.wide_bc), f);
+            bv[0] = pack(f[0], f[1]);
+            bv[1] = pack(f[2], f[3]);
+            unpack_quad(ld_quad(cp, PLAIN ? 4 : p.N - n0, PLAIN || p.wide_bc), f);
+            cv[0] = pack(f[0], f[1]);
+            cv[1] = pack(f[2], f[3]);
+        };
+        if (same_group) states(0);
         if (p.softplus) d = softplus_of(d);
-        float y = 0.f;
+        const float dx = d * x;
+        float y[I];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            if (cok && n0 + j < p.N) {
-                const float bv = Io<T>::ld((const T*)p.Bm + b * p.b_row + (long long)g * p.N + n0 + j);
-                const float cv = Io<T>::ld((const T*)p.Cm + b * p.c_row + (long long)g * p.N + n0 + j);
-                h[j] = fmaf(ex2(d * A2[j]), h[j], d * x * bv);
-                y = fmaf(h[j], cv, y);
+        for (int i = 0; i < I; ++i) {
+            if (!same_group) states(g[i]);
+            const f2 di = both(I == 1 ? d : __shfl_sync(all, d, base + i)), dxi = both(I == 1 ? dx : __shfl_sync(all, dx, base + i));
+            h[i][0] = fma2(ex2_2(mul2(di, A2[i][0])), h[i][0], mul2(dxi, bv[0]));
+            h[i][1] = fma2(ex2_2(mul2(di, A2[i][1])), h[i][1], mul2(dxi, bv[1]));
+            const float2 s = unpack(fma2(h[i][0], cv[0], mul2(h[i][1], cv[1])));
+            y[i] = s.x + s.y;
+        }
+        // sums over the channel's lanes; four channels are halved over the first four lanes
+        float o;
+        if constexpr (I == 4) {
+            const bool hi = nl & 2, up = nl & 1;
+            const float u = (hi ? y[2] : y[0]) + __shfl_xor_sync(all, hi ? y[0] : y[2], 2);
+            const float v = (hi ? y[3] : y[1]) + __shfl_xor_sync(all, hi ? y[1] : y[3], 2);
+            o = (up ? v : u) + __shfl_xor_sync(all, up ? u : v, 1);
+        } else if constexpr (I == 2) {
+            const bool up = nl & 1;
+            o = (up ? y[1] : y[0]) + __shfl_xor_sync(all, up ? y[0] : y[1], 1);
+            o += __shfl_xor_sync(all, o, 2);
+        } else {
+            o = y[0] + __shfl_xor_sync(all, y[0], 2);
+            o += __shfl_xor_sync(all, o, 1);
+        }
+#pragma unroll
+        for (int k = 4; k < NL; k *= 2) o += __shfl_xor_sync(all, o, k);
+        if (mine && nl < I) {
+            o = fmaf(D, x, o);
+            if (p.z) o *= silu(z);
+            Io<T>::st((T*)p.y + (long long)b * p.C + cm, o);
+        }
+    };
+
+    unsigned earlier = 0, later = 0;
+    if (idx) {
+        if (threadIdx.x < 2) flags[threadIdx.x] = 0;
+        __syncthreads();
+        for (int b = threadIdx.x; b < p.B; b += kStep) {
+            const int s = idx[b];
+            for (int r = 0; r < rows; ++r)
+                if (b != b0 + r && s == idx[b0 + r]) atomicOr(&flags[b > b0 + r], 1u << r);
+        }
+        __syncthreads();
+        earlier = flags[0];
+        later = flags[1];
+    }
+    for (int r = 0; r < rows; ++r) {
+        const int now = slot;
+#pragma unroll
+        for (int i = 0; i < I; ++i) {
+            h[i][0] = next[i][0];
+            h[i][1] = next[i][1];
+        }
+        slot = slot_of(r + 1);
+        fetch(slot);                                              // of no use to a row that leaves its token to another
+        if (now < 0 || now >= slots || (earlier >> r & 1)) continue;
+        token(b0 + r);
+        if (later >> r & 1) {
+            for (int b = b0 + r + 1; b < p.B; ++b)
+                if (idx[b] == now) token(b);
+        }
+        float* hp = p.h + (long long)now * p.C * p.N;
+#pragma unroll
+        for (int i = 0; i < I; ++i) {
+            if (!in[i]) continue;
+            float* to = hp + (at0 + i * at_step);
+            if (vec) {
+                if (PLAIN || n0 < p.N) *(ulonglong2*)to = make_ulonglong2(h[i][0], h[i][1]);
+            } else {
+                const float2 u = unpack(h[i][0]), v = unpack(h[i][1]);
+                const float f[4] = {u.x, u.y, v.x, v.y};
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (n0 + j < p.N) to[j] = f[j];
             }
         }
-        for (int o = NL / 2; o; o >>= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
-        if (cok && nl == 0) {
-            if (p.D) y = fmaf(p.D[c], x, y);
-            if (p.z) y *= silu(z);
-            Io<T>::st((T*)p.y + (long long)b * p.C + c, y);
-        }
-    }
-    if (vec && cok && n0 < p.N) {
-        *(float4*)hp = make_float4(h[0], h[1], h[2], h[3]);
-    } else {
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            if (cok && n0 + j < p.N) hp[j] = h[j];
     }
 }
 
@@ -1282,19 +1378,33 @@ gspn_status gspn_ssm_step(const gspn_ssm_desc* desc, const void* x, const void* 
     SsmArgs p;
     if (!make_args(desc, &p) || desc->L != 1 || desc->S != 0 || slots < 1) return GSPN_ERR_INVALID_ARG;
     if (!x || !dt || !A || !Bm || !Cm || !h || !y || (!idx && slots < p.B)) return GSPN_ERR_INVALID_ARG;
-    if (p.N > kMaxN || p.B > 65535) return GSPN_ERR_UNSUPPORTED;
+    if (p.N > kMaxN || p.B > 65535 || (long long)p.C * p.N >= (1 << 30)) return GSPN_ERR_UNSUPPORTED;
     const size_t es = dtype_size(desc->dtype);
     for (const void* q : {x, dt, Bm, Cm, z, (const void*)y})
         if (!aligned_to(q, es)) return GSPN_ERR_ALIGNMENT;
     for (const void* q : {(const void*)A, (const void*)D, (const void*)dt_bias, (const void*)idx, (const void*)h})
         if (!aligned_to(q, 4)) return GSPN_ERR_ALIGNMENT;
     p.x = x; p.dt = dt; p.z = z; p.Bm = Bm; p.Cm = Cm; p.A = A; p.D = D; p.bias = dt_bias; p.h = h; p.y = y;
-    p.wide = aligned_to(h, 16) && aligned_to(A, 16);
-    const int NL = lanes_for(p.N), threads = 128, ch = threads / NL;
-    const dim3 grid((p.C + ch - 1) / ch, p.B);
+    p.wide = p.N % 4 == 0 && aligned_to(h, 16) && aligned_to(A, 16);
+    p.wide_bc = p.N % 4 == 0 && wide_ok(Bm, p.b_row, 0, es) && wide_ok(Cm, p.c_row, 0, es);
+    // Four channels a lane where that leaves four blocks for each SM; rows share a block (and its reading
+    // of A) as far as eight remain.
+    const int NL = lanes_for(p.N);
+    const long long sms = device_sm_count(), wide_blocks = (p.C + 4 * kStep / NL - 1) / (4 * kStep / NL);
+    const bool four = wide_blocks * p.B >= 4 * sms;
+    const long long gx = four ? wide_blocks : (p.C + kStep / NL - 1) / (kStep / NL);
+    long long group = gx * p.B / (8 * sms);
+    group = group < 1 ? 1 : group > kGroup ? kGroup : group;
+    const dim3 grid((unsigned)gx, (unsigned)((p.B + group - 1) / group));
     cudaStream_t st = (cudaStream_t)stream;
-    if (desc->dtype == GSPN_F32) k_ssm_step<float><<<grid, threads, 0, st>>>(p, idx, slots, NL);
-    else k_ssm_step<__nv_bfloat16><<<grid, threads, 0, st>>>(p, idx, slots, NL);
+    with_lanes(desc->dtype, NL, [&](auto t, auto nl) {
+        using T = decltype(t);
+        constexpr int N = decltype(nl)::value;
+        auto go = [&](auto kernel) { kernel<<<grid, kStep, 0, st>>>(p, idx, slots, (int)group); };
+        const bool plain = p.G == 1 && p.N == 4 * N && p.wide && p.wide_bc && p.C % ((four ? 4 : 1) * kStep / N) == 0;
+        if (four) plain ? go(k_ssm_step<T, N, 4, true>) : go(k_ssm_step<T, N, 4, false>);
+        else plain ? go(k_ssm_step<T, N, 1, true>) : go(k_ssm_step<T, N, 1, false>);
+    });
     return last_status();
 }
 
