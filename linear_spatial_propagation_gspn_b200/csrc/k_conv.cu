@@ -11,9 +11,8 @@ namespace gspn {
 namespace seq {
 namespace {
 
-constexpr int kRunFwd = 16;     // tokens of a thread, forward
-constexpr int kRunBwd = 32;     // tokens of a thread, backward
-constexpr int kBatch = 4;       // tokens whose loads are in flight together
+constexpr int kRunFwd = 32, kRunBwd = 64;   // most tokens of a thread's run, forward and backward
+constexpr int kBatch = 4;       // tokens taken together
 constexpr int kVB = 4;          // channels of a thread
 
 struct ConvArgs {
@@ -88,6 +87,58 @@ __device__ __forceinline__ void st_pairs(T* p, const f2 (&v)[P], int n, bool wid
     st_ch<T, 2 * P>(p, f, n, wide);
 }
 
+// A thread's inputs on their way: tokens in batches of kBatch, S of them. WIDE: through places of its
+// own in shared memory (asynchronous copies that hold no registers while they are under way; only the
+// thread that copied them reads them, so there is no barrier); otherwise loaded when they are asked for.
+template <typename T, int P, bool WIDE, int S> struct Ring {
+    typedef typename Raw<T, P>::type R;
+    R (*at)[kBatch][128];        // [S][kBatch][thread]
+    const T* src;                // the next batch's tokens
+    long long step;
+    int left, n, put = 0, got = 0;
+    const T* now;                // the batch to be taken next (not WIDE)
+    __device__ __forceinline__ void issue() {
+        if constexpr (WIDE) {
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u) {
+                if (u < left) {
+                    const unsigned to = (unsigned)__cvta_generic_to_shared(&at[put][u][threadIdx.x]);
+                    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(to), "l"(src), "n"(sizeof(R)) : "memory");
+                }
+                src += step;
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+            put = put == S - 1 ? 0 : put + 1;
+            left -= kBatch;
+        }
+    }
+    __device__ __forceinline__ void begin(R (*smem)[kBatch][128], const T* p, long long tok, int tokens, int channels) {
+        at = smem;
+        src = now = p;
+        step = tok;
+        left = tokens;
+        n = channels;
+        put = got = 0;
+    }
+    // Takes the next batch (of the `tokens` that still come) and sends for the one S - 1 behind it. The
+    // groups of several rings of a thread have to be issued in turn.
+    template <int RINGS> __device__ __forceinline__ void take(R (&r)[kBatch], int tokens) {
+        if constexpr (WIDE) {
+            asm volatile("cp.async.wait_group %0;" ::"n"((S - 2) * RINGS) : "memory");
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u) r[u] = at[got][u][threadIdx.x];
+            got = got == S - 1 ? 0 : got + 1;
+        } else {
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u) {
+                r[u] = R{};
+                if (u < tokens) r[u] = ld_pairs_raw<T, P>(now, n, false);
+                now += step;
+            }
+        }
+    }
+};
+
 // The K - 1 inputs before token t of sequence s.
 template <typename T, int K, int P>
 __device__ __forceinline__ void window(const ConvArgs& p, const T* xr, const Seq& s, int t, int c, int n, f2 (&win)[K][P]) {
@@ -130,37 +181,37 @@ __device__ __forceinline__ void load_taps(const ConvArgs& p, int c, int n, f2 (&
 template <typename T, int K> __device__ void last_inputs(const ConvArgs& p, long long id);
 
 // Blocks behind the first `tokens` take the states behind the sequences.
-template <typename T, int K>
+template <typename T, int K, bool WIDE>
 __global__ void __launch_bounds__(128) k_conv_fwd(const ConvArgs p, long long blocks) {
     constexpr int P = kVB / 2;
+    constexpr int S = 4;
+    __shared__ __align__(16) typename Raw<T, P>::type smem[WIDE ? S : 1][kBatch][128];
     if (blockIdx.x >= blocks) {
         last_inputs<T, K>(p, (blockIdx.x - blocks) * (long long)blockDim.x + threadIdx.x);
         return;
     }
-    const long long id = (long long)blockIdx.x * blockDim.x + threadIdx.x;
-    const int cv = (int)(id % p.nvec);
-    const long long rr = id / p.nvec;
-    const int row = (int)(rr / p.runs);
+    const unsigned id = blockIdx.x * blockDim.x + threadIdx.x;    // under 2^31 (the host lengthens the runs for it)
+    const unsigned rr = id / (unsigned)p.nvec, cv = id - rr * p.nvec;
+    const int row = (int)(rr / (unsigned)p.runs);
     if (row >= p.B) return;
-    int t = (int)(rr % p.runs) * p.run;
+    int t = (int)(rr - row * (unsigned)p.runs) * p.run;
     const int te = min(t + p.run, p.L);
-    const int c = cv * kVB, n = p.C - c;
+    const int c = (int)cv * kVB, n = p.C - c;
     if (p.cu) t = max(t, cu_at(p, 0));
     if (t >= te) return;
     const T* xr = (const T*)p.x + row * p.x_row + c;
     T* yr = (T*)p.y + (long long)row * p.L * p.C + c;
-    typedef typename Raw<T, P>::type R;
-    R raw[kBatch], next[kBatch];
-    auto load = [&](int t) {
+    typename Raw<T, P>::type raw[kBatch];
+    T* py = yr + (long long)t * p.C;
+    Ring<T, P, WIDE, S> ring;
+    ring.begin(smem, xr + t * p.x_tok, p.x_tok, te - t, n);
 #pragma unroll
-        for (int u = 0; u < kBatch; ++u) next[u] = t + u < te ? ld_pairs_raw<T, P>(xr + (t + u) * p.x_tok, n, p.wide) : R{};
-    };
-    load(t);
+    for (int k = 0; k < S - 1; ++k) ring.issue();
     f2 w[K][P], b[P], win[K][P];
     load_taps<K, P>(p, c, n, w, b);
     Seq s = find(p, row, t);
     window<T, K, P>(p, xr, s, t, c, n, win);
-    auto one = [&](const R& q, int t) {
+    auto one = [&](const typename Raw<T, P>::type& q) {
         to_pairs(q, win[K - 1]);
         f2 o[P];
 #pragma unroll
@@ -172,15 +223,15 @@ __global__ void __launch_bounds__(128) k_conv_fwd(const ConvArgs p, long long bl
 #pragma unroll
             for (int k = 0; k < K - 1; ++k) win[k][i] = win[k + 1][i];
         }
-        st_pairs<T, P>(yr + (long long)t * p.C, o, n, p.wide);
+        st_pairs<T, P>(py, o, WIDE ? 2 * P : n, WIDE || p.wide);
+        py += p.C;
     };
     for (; t < te; t += kBatch) {
-#pragma unroll
-        for (int u = 0; u < kBatch; ++u) raw[u] = next[u];
-        load(t + kBatch);                                         // in flight while the present batch is worked on
+        ring.template take<1>(raw, te - t);
+        ring.issue();
         if (t + kBatch <= te && (!p.cu || (t + kBatch <= s.end && s.q < p.S))) {
 #pragma unroll
-            for (int u = 0; u < kBatch; ++u) one(raw[u], t + u);
+            for (int u = 0; u < kBatch; ++u) one(raw[u]);
         } else {
 #pragma unroll
             for (int u = 0; u < kBatch; ++u) {
@@ -190,7 +241,7 @@ __global__ void __launch_bounds__(128) k_conv_fwd(const ConvArgs p, long long bl
                     window<T, K, P>(p, xr, s, t + u, c, n, win);
                 }
                 if (p.cu && s.q >= p.S) return;                   // behind the last sequence
-                one(raw[u], t + u);
+                one(raw[u]);
             }
         }
     }
@@ -230,20 +281,21 @@ __global__ void k_conv_state(const ConvArgs p) {
 // runs in turn and keeps its sums of dw and dbias until the end; k_conv_sum adds the blocks in order.
 constexpr int kRows = 4;
 
-template <typename T, int K>
+template <typename T, int K, bool WIDE>
 __global__ void __launch_bounds__(128) k_conv_bwd(const ConvArgs p) {
     constexpr int P = kVB / 2;
-    __shared__ float red[kRows][K + 1][32 * kVB];
+    typedef typename Raw<T, P>::type R;
+    constexpr int S = sizeof(R) == 8 ? 4 : 2;                     // two rings of fp32 in 48 KB
+    __shared__ __align__(16) R smem[2][WIDE ? S : 1][kBatch][128];
+    __shared__ __align__(16) float red[kRows][K + 1][32 * kVB];
     const int lane = threadIdx.x & 31, grp = threadIdx.x >> 5;
     const int c = (blockIdx.x * 32 + lane) * kVB, n = p.C - c;
     const f2 zero = pack(0.f, 0.f);
-    f2 w[K][P], b[P], dw[K][P], db[P];
+    f2 w[K][P], b[P];
+    // the thread's sums of dw and dbias over its runs: its own places, so no barrier is needed
+    auto total = [&](int k) -> ulonglong2& { return *(ulonglong2*)&red[grp][k][lane * kVB]; };
 #pragma unroll
-    for (int i = 0; i < P; ++i) {
-        db[i] = zero;
-#pragma unroll
-        for (int k = 0; k < K; ++k) dw[k][i] = zero;
-    }
+    for (int k = 0; k <= K; ++k) total(k) = make_ulonglong2(zero, zero);
     if (n > 0) {
         load_taps<K, P>(p, c, n, w, b);
         const long long all = (long long)p.B * p.runs;
@@ -259,16 +311,16 @@ __global__ void __launch_bounds__(128) k_conv_bwd(const ConvArgs p) {
             Seq s = find(p, row, ta);
             if (p.cu && s.q >= p.S) continue;
             const int stop = min(tb + K - 1, p.L);
-            typename Raw<T, P>::type xs[kBatch], gs[kBatch], xn[kBatch], gn[kBatch];
-            auto load = [&](int t) {
+            R xs[kBatch], gs[kBatch];
+            T* pd = dr + (long long)(ta - (K - 1)) * p.C;         // where token t - (K - 1) goes
+            Ring<T, P, WIDE, S> rx, rg;
+            rx.begin(smem[0], xr + ta * p.x_tok, p.x_tok, stop - ta, n);
+            rg.begin(smem[1], gr + (long long)ta * p.C, p.C, stop - ta, n);
 #pragma unroll
-                for (int u = 0; u < kBatch; ++u) {
-                    const bool in = t + u < stop;
-                    xn[u] = ld_pairs_raw<T, P>(xr + (in ? (t + u) * p.x_tok : 0), in ? n : 0, p.wide);
-                    gn[u] = ld_pairs_raw<T, P>(gr + (in ? (long long)(t + u) * p.C : 0), in ? n : 0, p.wide);
-                }
-            };
-            load(ta);
+            for (int k = 0; k < S - 1; ++k) {
+                rx.issue();
+                rg.issue();
+            }
             f2 win[K][P], acc[K][P], run_dw[K][P], run_db[P];
             window<T, K, P>(p, xr, s, ta, c, n, win);
 #pragma unroll
@@ -325,19 +377,22 @@ __global__ void __launch_bounds__(128) k_conv_bwd(const ConvArgs p) {
             };
             bool open = true;
             for (int t = ta; open && t < stop; t += kBatch) {
-#pragma unroll
-                for (int u = 0; u < kBatch; ++u) { xs[u] = xn[u]; gs[u] = gn[u]; }
-                load(t + kBatch);
+                rx.template take<2>(xs, stop - t);
+                rg.template take<2>(gs, stop - t);
+                rx.issue();
+                rg.issue();
                 if (t >= max(ta, s.start) + K - 1 && t + kBatch <= min(tb, s.end)) {
                     // all within the run and one sequence: every token completes one that the run owns
 #pragma unroll
                     for (int u = 0; u < kBatch; ++u) {
                         one(u, true);
-                        st_pairs<T, P>(dr + (long long)(t + u - (K - 1)) * p.C, acc[0], n, p.wide);
+                        st_pairs<T, P>(pd, acc[0], WIDE ? 2 * P : n, WIDE || p.wide);
+                        pd += p.C;
                         shift();
                     }
                     continue;
                 }
+                pd += (long long)kBatch * p.C;
 #pragma unroll
                 for (int u = 0; u < kBatch; ++u) {
                     const int tt = t + u;
@@ -367,19 +422,11 @@ __global__ void __launch_bounds__(128) k_conv_bwd(const ConvArgs p) {
                 for (int k = 0; k < K - 1; ++k) put(stop - (K - 1) + k, acc[k]);
             }
 #pragma unroll
-            for (int i = 0; i < P; ++i) {
-                db[i] = add2(db[i], run_db[i]);
-#pragma unroll
-                for (int k = 0; k < K; ++k) dw[k][i] = add2(dw[k][i], run_dw[k][i]);
+            for (int k = 0; k <= K; ++k) {
+                ulonglong2& s = total(k);
+                s = make_ulonglong2(add2(s.x, k < K ? run_dw[k < K ? k : 0][0] : run_db[0]),
+                                    add2(s.y, k < K ? run_dw[k < K ? k : 0][1] : run_db[1]));
             }
-        }
-    }
-#pragma unroll
-    for (int i = 0; i < P; ++i) {
-#pragma unroll
-        for (int k = 0; k <= K; ++k) {
-            const float2 v = unpack(k < K ? dw[k][i] : db[i]);
-            *(float2*)&red[grp][k][lane * kVB + 2 * i] = v;
         }
     }
     __syncthreads();
@@ -560,11 +607,21 @@ bool fits(const gspn_conv_desc& d) {
     return d.L <= (1 << 30) && (long long)d.B * d.L <= (1LL << 31) - 1 && (long long)d.C * (d.K + 1) < (1LL << 30) &&
            (long long)d.B * d.L / 4 * d.C < (1LL << 36) && seqs * d.C < (1LL << 36);
 }
+// Tokens of a run: `most`, halved while fewer than 192 threads would be there for each SM (`lines` threads
+// side by side). Short runs read K - 1 inputs and the filters more often: 2048 tokens of 1024 channels
+// took 6.2 us in runs of 16 and 8.3 in runs of 4.
+int run_for(long long lines, int L, int most) {
+    int run = most;
+    while (run > kBatch && lines * ((L + run - 1) / run) < 192LL * device_sm_count()) run /= 2;
+    return run;
+}
+int run_bwd(const gspn_conv_desc& d) { return run_for((long long)d.B * ((d.C + kVB - 1) / kVB), d.L, kRunBwd); }
 // Blocks along the tokens of the backward pass: enough to fill the SMs eight times, no more than there
 // are groups of runs.
 int bwd_blocks(const gspn_conv_desc& d) {
     const long long gx = (d.C + 32 * kVB - 1) / (32 * kVB);
-    const long long groups = ((long long)d.B * ((d.L + kRunBwd - 1) / kRunBwd) + kRows - 1) / kRows;
+    const int run = run_bwd(d);
+    const long long groups = ((long long)d.B * ((d.L + run - 1) / run) + kRows - 1) / kRows;
     long long gy = (8LL * device_sm_count() + gx - 1) / gx;
     gy = gy < groups ? gy : groups;
     gy = gy < 65535 ? gy : 65535;
@@ -613,11 +670,11 @@ gspn_status gspn_conv_forward(const gspn_conv_desc* desc, const void* x, const f
     p.wide = (p.C * es) % 16 == 0 && wide_ok(x, p.x_row, p.x_tok, es) && aligned_to(y, 16) && aligned_to(state0, 16);
     p.wide_w = aligned_to(w, 16);
     p.nvec = (p.C + kVB - 1) / kVB;
-    // Short inputs are cut into runs of kBatch tokens, so that more threads share them.
-    const long long threads16 = (long long)p.B * ((p.L + kRunFwd - 1) / kRunFwd) * p.nvec;
-    p.run = threads16 >= 1024LL * device_sm_count() ? kRunFwd : kBatch;
+    p.run = run_for((long long)p.B * p.nvec, p.L, kRunFwd);
+    while ((long long)p.B * ((p.L + p.run - 1) / p.run) * p.nvec >= (1LL << 31) - 128 && p.run < p.L) p.run *= 2;
     p.runs = (p.L + p.run - 1) / p.run;
     const long long total = (long long)p.B * p.runs * p.nvec;
+    if (total >= (1LL << 31) - 128) return GSPN_ERR_UNSUPPORTED;
     cudaStream_t st = (cudaStream_t)stream;
     with_taps(desc->dtype, desc->K, [&](auto t, auto k) {
         using T = decltype(t);
@@ -625,7 +682,8 @@ gspn_status gspn_conv_forward(const gspn_conv_desc* desc, const void* x, const f
         const long long blocks = (total + 127) / 128, behind = state ? ((long long)p.S * p.C + 127) / 128 : 0;
         const bool apart = state == state0;                       // no thread of this launch may still read state0
         if (blocks + (apart ? 0 : behind) > 0)
-            k_conv_fwd<T, K><<<(unsigned)(blocks + (apart ? 0 : behind)), 128, 0, st>>>(p, blocks);
+            p.wide ? k_conv_fwd<T, K, true><<<(unsigned)(blocks + (apart ? 0 : behind)), 128, 0, st>>>(p, blocks)
+                   : k_conv_fwd<T, K, false><<<(unsigned)(blocks + (apart ? 0 : behind)), 128, 0, st>>>(p, blocks);
         if (apart && behind > 0) k_conv_state<T, K><<<(unsigned)behind, 128, 0, st>>>(p);
     });
     return last_status();
@@ -653,15 +711,15 @@ gspn_status gspn_conv_backward(const gspn_conv_desc* desc, const void* x, const 
     p.wide = (p.C * es) % 16 == 0 && wide_ok(x, p.x_row, p.x_tok, es) && aligned_to(dy, 16) && aligned_to(dx, 16) &&
              aligned_to(state0, 16) && aligned_to(dstate, 16);
     p.wide_w = aligned_to(w, 16);
-    p.run = kRunBwd;
-    p.runs = (p.L + kRunBwd - 1) / kRunBwd;
+    p.run = run_bwd(*desc);
+    p.runs = (p.L + p.run - 1) / p.run;
     const int gy = bwd_blocks(*desc);
     cudaStream_t st = (cudaStream_t)stream;
     with_taps(desc->dtype, desc->K, [&](auto t, auto k) {
         using T = decltype(t);
         constexpr int K = decltype(k)::value;
         const dim3 grid((p.C + 32 * kVB - 1) / (32 * kVB), gy);
-        k_conv_bwd<T, K><<<grid, 128, 0, st>>>(p);
+        p.wide ? k_conv_bwd<T, K, true><<<grid, 128, 0, st>>>(p) : k_conv_bwd<T, K, false><<<grid, 128, 0, st>>>(p);
         k_conv_sum<<<((K + 1) * p.C + 31) / 32, dim3(32, 8), 0, st>>>(p.part, gy, p.C, K, dw, dbias);
         if (dstate0) {
             const long long n = (long long)p.S * p.C;
