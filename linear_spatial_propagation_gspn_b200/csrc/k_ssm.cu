@@ -846,24 +846,41 @@ __global__ void __launch_bounds__(kScan + kFeedB, 1) k_ssm_bwd(const SsmArgs p) 
             }
         };
         fetch(kTB - 1);
+        // A token's sums over lanes take three exchanges in turn. They run beside the next token's arithmetic,
+        // a level at a time: a scheduler has this one scanning warp, which issues in order and would
+        // otherwise wait out each exchange.
+        f2 pB[2], pC[2];                                          // of the token ahead: shares of dB and dC,
+        float py[2], pg[2], pe[2];                                // and of the sums over n
 #pragma unroll
-        for (int t = kTB - 1; t >= 0; --t) {
-            if (t > 0) fetch(t - 1);
-            const f2 (&b2)[2] = ob[t & 1];
-            const f2 (&c2)[2] = oc2[t & 1];
+        for (int t = kTB - 1; t >= -1; --t) {
+            const bool work = t >= 0, sums = t < kTB - 1;
+            float x0, x1, x2, x3, xy, xg, xe;                     // what comes back from the first exchange
+            float vb = 0.f, vb2 = 0.f, vc = 0.f, vc2 = 0.f, y1 = 0.f, y2 = 0.f, z1 = 0.f;
+            if (sums) {
+                x0 = __shfl_xor_sync(all, unpack(pB[0]).y, NL);
+                x1 = __shfl_xor_sync(all, unpack(pB[1]).y, NL);
+                x2 = __shfl_xor_sync(all, unpack(pC[0]).y, NL);
+                x3 = __shfl_xor_sync(all, unpack(pC[1]).y, NL);
+                xy = __shfl_xor_sync(all, py[1], 1);              // slot 1 is the neighbour's slot 0
+                xg = __shfl_xor_sync(all, pg[1], 1);
+                xe = __shfl_xor_sync(all, pe[1], 1);
+            }
             f2 vB[2], vC[2];
             float yv[2], gv[2], ev[2];
-#pragma unroll
-            for (int s = 0; s < 2; ++s) {
+            auto slot = [&](auto which) {
+                constexpr int s = decltype(which)::value;
+                const f2 (&b2)[2] = ob[t & 1];
+                const f2 (&c2)[2] = oc2[t & 1];
                 const f2 d = od[t & 1][s], dx = odx[t & 1][s], r = orr[t & 1][s];
                 f2 y, gb, ea;
 #pragma unroll
                 for (int m = 0; m < 2; ++m) {
-                    const f2 hp = t ? h[t - 1][s][m] : hin[s][m];
+                    const f2 hp = t > 0 ? h[t > 0 ? t - 1 : 0][s][m] : hin[s][m];
+                    const f2 ht = h[t > 0 ? t : 0][s][m];
                     const f2 g = fma2(c2[m], r, ag[s][m]);
-                    vC[m] = s ? fma2(r, h[t][s][m], vC[m]) : mul2(r, h[t][s][m]);
+                    vC[m] = s ? fma2(r, ht, vC[m]) : mul2(r, ht);
                     vB[m] = s ? fma2(g, dx, vB[m]) : mul2(g, dx);
-                    y = m ? fma2(c2[m], h[t][s][m], y) : mul2(c2[m], h[t][s][m]);
+                    y = m ? fma2(c2[m], ht, y) : mul2(c2[m], ht);
                     gb = m ? fma2(g, b2[m], gb) : mul2(g, b2[m]);
                     ag[s][m] = mul2(ex2_2(mul2(d, A2[s][m])), g);
                     const f2 e = mul2(ag[s][m], hp);
@@ -874,32 +891,53 @@ __global__ void __launch_bounds__(kScan + kFeedB, 1) k_ssm_bwd(const SsmArgs p) 
                 yv[s] = u.x + u.y;
                 gv[s] = v.x + v.y;
                 ev[s] = w.x + w.y;
+            };
+            if (work) {
+                if (t > 0) fetch(t - 1);
+                slot(std::integral_constant<int, 0>());
             }
-            // slot 1 is the neighbour's slot 0
-            const int oc = ORow<NL>::at(cl[0], nl >> 1);
-            sm.o[buf][0][t][oc] = yv[0] + __shfl_xor_sync(all, yv[1], 1);
-            sm.o[buf][1][t][oc] = gv[0] + __shfl_xor_sync(all, gv[1], 1);
-            sm.o[buf][2][t][oc] = ev[0] + __shfl_xor_sync(all, ev[1], 1);
-            // sums over the warp's channels
-            float* out = sm.sum[buf][warp][t];
-            const float2 B0 = unpack(vB[0]), B1 = unpack(vB[1]), C0 = unpack(vC[0]), C1 = unpack(vC[1]);
-            float vb = B0.x + __shfl_xor_sync(all, B0.y, NL), vb2 = B1.x + __shfl_xor_sync(all, B1.y, NL);
-            float vc = C0.x + __shfl_xor_sync(all, C0.y, NL), vc2 = C1.x + __shfl_xor_sync(all, C1.y, NL);
-            if constexpr (NL == 16) {
-                out[n0 + pm] = vb;
-                out[n0 + (2 ^ pm)] = vb2;
-                out[4 * NL + n0 + pm] = vc;
-                out[4 * NL + n0 + (2 ^ pm)] = vc2;
-            } else {
-                vb += __shfl_xor_sync(all, vb2, 2 * NL);
-                vc += __shfl_xor_sync(all, vc2, 2 * NL);
-                if constexpr (NL == 8) {
-                    out[n0 + pm] = vb;
-                    out[4 * NL + n0 + pm] = vc;
-                } else {
-                    const bool up = ql & 4;
-                    out[(up ? 4 * NL : 0) + n0 + pm] = (up ? vc : vb) + __shfl_xor_sync(all, up ? vb : vc, 4 * NL);
+            float* out = sm.sum[buf][warp][sums ? t + 1 : 0];
+            if (sums) {
+                vb = unpack(pB[0]).x + x0;
+                vb2 = unpack(pB[1]).x + x1;
+                vc = unpack(pC[0]).x + x2;
+                vc2 = unpack(pC[1]).x + x3;
+                if constexpr (NL < 16) {
+                    y1 = __shfl_xor_sync(all, vb2, 2 * NL);
+                    y2 = __shfl_xor_sync(all, vc2, 2 * NL);
                 }
+                const int oc = ORow<NL>::at(cl[0], nl >> 1);
+                sm.o[buf][0][t + 1][oc] = py[0] + xy;
+                sm.o[buf][1][t + 1][oc] = pg[0] + xg;
+                sm.o[buf][2][t + 1][oc] = pe[0] + xe;
+            }
+            if (work) slot(std::integral_constant<int, 1>());
+            if (sums) {
+                if constexpr (NL == 16) {
+                    out[n0 + pm] = vb;
+                    out[n0 + (2 ^ pm)] = vb2;
+                    out[4 * NL + n0 + pm] = vc;
+                    out[4 * NL + n0 + (2 ^ pm)] = vc2;
+                } else {
+                    vb += y1;
+                    vc += y2;
+                    if constexpr (NL == 8) {
+                        out[n0 + pm] = vb;
+                        out[4 * NL + n0 + pm] = vc;
+                    } else {
+                        const bool up = ql & 4;
+                        z1 = __shfl_xor_sync(all, up ? vb : vc, 4 * NL);
+                        out[(up ? 4 * NL : 0) + n0 + pm] = (up ? vc : vb) + z1;
+                    }
+                }
+            }
+#pragma unroll
+            for (int m = 0; m < 2; ++m) {
+                pB[m] = vB[m];
+                pC[m] = vC[m];
+                py[m] = yv[m];
+                pg[m] = gv[m];
+                pe[m] = ev[m];
             }
         }
 #pragma unroll
