@@ -39,7 +39,7 @@ struct NormArgs {
 // of a row whose tensors are aligned in different ways, go element by element.
 struct Row {
     int C, tid, tpr, phase;
-    bool wide;
+    bool wide, edge;             // edge: a thread of the warp has columns outside the row
 };
 template <typename T, int E> struct Lay {
     static constexpr int V = Vec<T>::V, H = E / 2, K = E / V;
@@ -50,9 +50,11 @@ template <typename T, typename S, int E> struct RowRaw {
     static constexpr int W = Vec<T>::V * sizeof(S) / 4;           // words of a vector
     uint32_t q[E / Vec<T>::V][W];
 };
+template <typename T, int E>
+__device__ __forceinline__ bool inside(const Row& w, int e) { return (unsigned)Lay<T, E>::col(w, e) < (unsigned)w.C; }
 // A vector that crosses an end of the row is loaded whole all the same, where its other columns are those
-// of rows around (before it they always are; `more`: seven elements follow behind the row too), and
-// those are set to zero.
+// of rows around (before it they always are; `more`: seven elements follow behind the row too);
+// clear_row sets those to zero. Threads whose columns all lie behind the row keep the zeros they began with.
 template <typename T, typename S, int E>
 __device__ __forceinline__ void ld_row(RowRaw<T, S, E>& r, const S* p, const Row& w, bool more) {
     using Y = Lay<T, E>;
@@ -60,7 +62,8 @@ __device__ __forceinline__ void ld_row(RowRaw<T, S, E>& r, const S* p, const Row
 #pragma unroll
     for (int k = 0; k < Y::K; ++k) {
         const int c = Y::col(w, k * V);
-        if (w.wide && c < w.C && (more || c + V <= w.C)) {
+        if (c >= w.C) continue;
+        if (w.wide && (more || c + V <= w.C)) {
             if constexpr (W == 2) {
                 const uint2 v = *(const uint2*)(p + c);
                 r.q[k][0] = v.x; r.q[k][1] = v.y;
@@ -71,30 +74,31 @@ __device__ __forceinline__ void ld_row(RowRaw<T, S, E>& r, const S* p, const Row
                     r.q[k][m] = v.x; r.q[k][m + 1] = v.y; r.q[k][m + 2] = v.z; r.q[k][m + 3] = v.w;
                 }
             }
-            if (c < 0 || c + V > w.C) {
-#pragma unroll
-                for (int j = 0; j < W; ++j) {
-                    if constexpr (sizeof(S) == 4) {
-                        if (c + j < 0 || c + j >= w.C) r.q[k][j] = 0u;
-                    } else {
-                        const int c0 = c + 2 * j, c1 = c0 + 1;
-                        r.q[k][j] &= (c0 >= 0 && c0 < w.C ? 0xffffu : 0u) | (c1 >= 0 && c1 < w.C ? 0xffff0000u : 0u);
-                    }
-                }
-            }
         } else {
 #pragma unroll
             for (int j = 0; j < W; ++j) {
                 if constexpr (sizeof(S) == 4) {
-                    const int cc = c + j;
-                    r.q[k][j] = cc >= 0 && cc < w.C ? ((const uint32_t*)p)[cc] : 0u;
+                    r.q[k][j] = inside<T, E>(w, k * V + j) ? ((const uint32_t*)p)[c + j] : 0u;
                 } else {
-                    const int c0 = c + 2 * j, c1 = c0 + 1;
-                    const uint32_t lo = c0 >= 0 && c0 < w.C ? ((const uint16_t*)p)[c0] : 0u;
-                    const uint32_t hi = c1 >= 0 && c1 < w.C ? ((const uint16_t*)p)[c1] : 0u;
+                    const uint32_t lo = inside<T, E>(w, k * V + 2 * j) ? ((const uint16_t*)p)[c + 2 * j] : 0u;
+                    const uint32_t hi = inside<T, E>(w, k * V + 2 * j + 1) ? ((const uint16_t*)p)[c + 2 * j + 1] : 0u;
                     r.q[k][j] = lo | hi << 16;
                 }
             }
+        }
+    }
+}
+template <typename T, typename S, int E>
+__device__ __forceinline__ void clear_row(RowRaw<T, S, E>& r, const Row& w) {
+    constexpr int V = Vec<T>::V;
+#pragma unroll
+    for (int e = 0; e < E; e += 2) {
+        const uint32_t a = inside<T, E>(w, e) ? ~0u : 0u, b = inside<T, E>(w, e + 1) ? ~0u : 0u;
+        if constexpr (sizeof(S) == 4) {
+            r.q[e / V][e % V] &= a;
+            r.q[e / V][e % V + 1] &= b;
+        } else {
+            r.q[e / V][e % V / 2] &= (a & 0xffffu) | (b & 0xffff0000u);
         }
     }
 }
@@ -127,7 +131,7 @@ __device__ __forceinline__ void st_row(S* p, const Row& w, const f2 (&v)[E / 2])
         } else {
 #pragma unroll
             for (int j = 0; j < V; ++j)
-                if (c + j >= 0 && c + j < w.C) Io<S>::st(p + c + j, f[j]);
+                if (inside<T, E>(w, k * V + j)) Io<S>::st(p + c + j, f[j]);
         }
     }
 }
@@ -155,10 +159,11 @@ template <typename T, int E> struct Params {
 };
 
 // Sums over the threads of a row: the lanes of a warp, or (WARP = false) the warps of the block as well.
-// Three buffers in turn, so that one barrier a call is enough.
+// Three buffers in turn, so that one barrier a call is enough. Four sums cost little more than one: the
+// lanes share them out by halves.
 template <bool WARP>
 struct RowSum {
-    float (*buf)[2][32];
+    float (*buf)[4][8];          // [turn][sum][warp]
     int turn = 0;
     __device__ __forceinline__ float one(float a) {
 #pragma unroll
@@ -170,31 +175,37 @@ struct RowSum {
         turn = turn == 2 ? 0 : turn + 1;
         return a;
     }
-    // two sums at once: half of the lanes go on with each
-    __device__ __forceinline__ float2 two(float a, float b) {
-        const bool up = threadIdx.x & 16;
-        float v = (up ? b : a) + __shfl_xor_sync(0xffffffffu, up ? a : b, 16);
+    __device__ __forceinline__ float4 four(float a, float b, float c, float d) {
+        constexpr unsigned all = 0xffffffffu;
+        const bool up = threadIdx.x & 16, hi = threadIdx.x & 8;
+        const float x = (up ? b : a) + __shfl_xor_sync(all, up ? a : b, 16);
+        const float y = (up ? d : c) + __shfl_xor_sync(all, up ? c : d, 16);
+        float v = (hi ? y : x) + __shfl_xor_sync(all, hi ? x : y, 8);
 #pragma unroll
-        for (int o = 8; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+        for (int o = 4; o; o >>= 1) v += __shfl_xor_sync(all, v, o);
+        float4 s;
         if constexpr (WARP) {
-            const float w = __shfl_xor_sync(0xffffffffu, v, 16);
-            return up ? make_float2(w, v) : make_float2(v, w);
+            s.x = __shfl_sync(all, v, 0);
+            s.y = __shfl_sync(all, v, 16);
+            s.z = __shfl_sync(all, v, 8);
+            s.w = __shfl_sync(all, v, 24);
+        } else {
+            if ((threadIdx.x & 7) == 0) buf[turn][(up ? 1 : 0) + (hi ? 2 : 0)][threadIdx.x >> 5] = v;
+            __syncthreads();
+            s.x = over_warps(0);
+            s.y = over_warps(1);
+            s.z = over_warps(2);
+            s.w = over_warps(3);
+            turn = turn == 2 ? 0 : turn + 1;
         }
-        if ((threadIdx.x & 15) == 0) buf[turn][up][threadIdx.x >> 5] = v;
-        __syncthreads();
-        const float2 s = make_float2(over_warps(0), over_warps(1));
-        turn = turn == 2 ? 0 : turn + 1;
         return s;
     }
+    // eight warps at most; the places of those that are not there hold zeros
     __device__ __forceinline__ float over_warps(int i) const {
-        const int warps = blockDim.x >> 5;
-        f2 s = both(0.f);
-        for (int w = 0; w < warps; w += 4) {                      // places behind the last warp hold zeros
-            f2 x, y;
-            ld_pairs(&buf[turn][i][w], x, y);
-            s = add2(s, add2(x, y));
-        }
-        const float2 v = unpack(s);
+        f2 a, b, c, d;
+        ld_pairs(&buf[turn][i][0], a, b);
+        ld_pairs(&buf[turn][i][4], c, d);
+        const float2 v = unpack(add2(add2(a, b), add2(c, d)));
         return v.x + v.y;
     }
 };
@@ -215,31 +226,26 @@ __device__ __forceinline__ float dot_all(const f2 (&v)[H], const f2 (&w)[H]) {
     return f.x + f.y;
 }
 
-// Takes v to its normalised form in place; returns one over its spread.
-template <typename T, int E, bool WARP>
-__device__ __forceinline__ float to_unit(f2 (&v)[E / 2], const NormArgs& p, const Row& w, RowSum<WARP>& sum) {
-    using Y = Lay<T, E>;
-    if (p.center) {
-        const f2 mean = both(-sum.one(sum_all(v)) * p.inv_c);
+// Takes the mean off; places that are no columns stay zero.
+template <typename T, int E>
+__device__ __forceinline__ void shift_row(f2 (&v)[E / 2], float mean, const Row& w) {
+    const f2 by = both(-mean);
 #pragma unroll
-        for (int k = 0; k < Y::K; ++k) {
-            const int c = Y::col(w, k * Y::V);
-            const bool inside = c >= 0 && c + Y::V <= w.C;
+    for (int k = 0; k < E / 2; ++k) v[k] = add2(v[k], by);
+    if (w.edge)
 #pragma unroll
-            for (int j = 0; j < Y::V; j += 2) {
-                f2& x = v[(k * Y::V + j) / 2];
-                x = add2(x, mean);
-                if (!inside) {                                    // places that are no columns stay zero
-                    const float2 f = unpack(x);
-                    x = pack(c + j >= 0 && c + j < w.C ? f.x : 0.f, c + j + 1 >= 0 && c + j + 1 < w.C ? f.y : 0.f);
-                }
-            }
+        for (int k = 0; k < E / 2; ++k) {
+            const float2 f = unpack(v[k]);
+            v[k] = pack(inside<T, E>(w, 2 * k) ? f.x : 0.f, inside<T, E>(w, 2 * k + 1) ? f.y : 0.f);
         }
-    }
+}
+// Takes v to its normalised form in place.
+template <typename T, int E, bool WARP>
+__device__ __forceinline__ void to_unit(f2 (&v)[E / 2], const NormArgs& p, const Row& w, RowSum<WARP>& sum) {
+    if (p.center) shift_row<T, E>(v, sum.one(sum_all(v)) * p.inv_c, w);
     const float rs = rsqrtf(fmaf(sum.one(dot_all(v, v)), p.inv_c, p.eps));
 #pragma unroll
     for (int k = 0; k < E / 2; ++k) v[k] = mul2(v[k], both(rs));
-    return rs;
 }
 
 template <typename T, int E>
@@ -270,10 +276,11 @@ __device__ __forceinline__ Row place(const NormArgs& p, long long& row, long lon
     step = WARP ? (long long)gridDim.x * 4 : gridDim.x;
     w.wide = p.wide;
     w.phase = p.wide ? (int)(row * p.C % Lay<T, E>::V) : 0;
+    w.edge = __any_sync(0xffffffffu, !inside<T, E>(w, 0) || !inside<T, E>(w, E - 1));
     return w;
 }
 template <typename T, int E, bool WARP>
-__device__ __forceinline__ Params<T, E> params(const NormArgs& p, const Row& w, float* smem, float (*buf)[2][32]) {
+__device__ __forceinline__ Params<T, E> params(const NormArgs& p, const Row& w, float* smem, float (*buf)[4][8]) {
     Params<T, E> q{smem + (WARP ? (threadIdx.x >> 5) * kParams * 32 * E : 0), w.tpr * E};
     q.put(kWPost, p.w_post, w);
     q.put(kBPost, p.b_post, w);
@@ -282,7 +289,7 @@ __device__ __forceinline__ Params<T, E> params(const NormArgs& p, const Row& w, 
     q.put(kBPre, p.b_pre, w);
     if constexpr (!WARP) {
         if (threadIdx.x < 32)
-            for (int i = 0; i < 6; ++i) buf[i / 2][i % 2][threadIdx.x] = 0.f;
+            for (int i = 0; i < 3; ++i) buf[i][threadIdx.x / 8][threadIdx.x % 8] = 0.f;
         __syncthreads();
     }
     return q;
@@ -293,7 +300,7 @@ __device__ __forceinline__ Params<T, E> params(const NormArgs& p, const Row& w, 
 template <typename T, typename R, int E, int MAXT, bool WARP = MAXT == 128>
 __global__ void __launch_bounds__(MAXT, MAXT == 128 ? 1 : E == 8 ? 4 : 2) k_norm_fwd(const NormArgs p) {
     constexpr int H = E / 2;
-    __shared__ __align__(16) float buf[3][2][32];
+    __shared__ __align__(16) float buf[3][4][8];
     extern __shared__ __align__(16) float smem[];
     RowSum<WARP> sum{buf};
     long long row, step;
@@ -310,6 +317,11 @@ __global__ void __launch_bounds__(MAXT, MAXT == 128 ? 1 : E == 8 ? 4 : 2) k_norm
     if (row < p.rows) load(row);
     for (; row < p.rows; row += step) {
         f2 m[H], r[H], g[H];
+        if (w.edge) {
+            clear_row<T, T, E>(ny, w);
+            clear_row<T, R, E>(nr, w);
+            clear_row<T, T, E>(ng, w);
+        }
         open_row<T, T, E>(ny, m);
         open_row<T, R, E>(nr, r);
         open_row<T, T, E>(ng, g);
@@ -336,16 +348,16 @@ __global__ void __launch_bounds__(MAXT, MAXT == 128 ? 1 : E == 8 ? 4 : 2) k_norm
 
 // Backward of one norm: g = gradient of its normalised form (already times the weight) is taken in
 // place to the gradient of its input: (g - unit mean(g unit) - mean(g)) / spread, the last mean only
-// when centred. Places that are no columns end up with -mean(g) / spread: the next weight is zero there,
-// and they are never stored.
-template <int H, bool WARP>
-__device__ __forceinline__ void unit_back(f2 (&g)[H], const f2 (&unit)[H], float rs, const NormArgs& p, RowSum<WARP>& sum) {
-    const float a = dot_all(g, unit);
-    const float2 s = p.center ? sum.two(a, sum_all(g)) : make_float2(sum.one(a), 0.f);
-    const f2 ma = both(-s.x * p.inv_c), mb = both(-s.y * p.inv_c), k2 = both(rs);
+// when centred. `gu`, `gs`: the sums of g unit and of g. Places that are no columns end up with
+// -mean(g) / spread: the next weight is zero there, and they are never stored.
+template <int H>
+__device__ __forceinline__ void unit_back(f2 (&g)[H], const f2 (&unit)[H], float rs, float gu, float gs, const NormArgs& p) {
+    const f2 ma = both(-gu * p.inv_c), mb = both(-gs * p.inv_c), k2 = both(rs);
 #pragma unroll
     for (int k = 0; k < H; ++k) g[k] = mul2(add2(g[k], fma2(unit[k], ma, mb)), k2);
 }
+
+__device__ __forceinline__ float2 pair_of(float4 v) { return make_float2(v.x, v.y); }
 
 // Column sums over the rows of a block, in registers: a thread's columns are its own.
 template <int H> struct Cols {
@@ -372,7 +384,7 @@ template <typename T, typename R, int E, int MAXT, bool WARP = MAXT == 128>
 __global__ void __launch_bounds__(MAXT, MAXT == 256 && E == 8 ? 2 : 1) k_norm_bwd(const NormArgs p) {
     using Y = Lay<T, E>;
     constexpr int H = E / 2;
-    __shared__ __align__(16) float buf[3][2][32];
+    __shared__ __align__(16) float buf[3][4][8];
     extern __shared__ __align__(16) float smem[];
     RowSum<WARP> sum{buf};
     long long row, step;
@@ -396,30 +408,61 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 && E == 8 ? 2 : 1) k_norm_bw
     for (; row < p.rows; row += step) {
         f2 d[H], y[H], g[H];                                      // d: the gradient of r_out
         f2 u[H], go[H];
+        if (w.edge) {
+            clear_row<T, T, E>(ny, w);
+            clear_row<T, T, E>(ng, w);
+            clear_row<T, R, E>(nd, w);
+            clear_row<T, R, E>(nu, w);
+            clear_row<T, T, E>(no, w);
+        }
         open_row<T, T, E>(ny, y);
         open_row<T, T, E>(ng, g);
         open_row<T, R, E>(nd, d);
         open_row<T, R, E>(nu, u);
         open_row<T, T, E>(no, go);
         if (row + step < p.rows) load(row + step);
-        if (p.w_pre) {
-            const float rs = to_unit<T, E, WARP>(u, p, w, sum);
-            cols.template add<kDbPre>(p.slot[kDbPre], go);
-            cols.template add_product<kDwPre>(p.slot[kDwPre], go, u);
-            scale_by<T, E>(go, prm, kWPre, w);
-            unit_back<H, WARP>(go, u, rs, p, sum);
-#pragma unroll
-            for (int k = 0; k < H; ++k) d[k] = add2(d[k], go[k]);
-        }
-        if (p.dr_in) st_row<T, R, E>((R*)p.dr_in + row * p.C, w, d);
         f2 m[H], s[H];
 #pragma unroll
         for (int k = 0; k < H; ++k) {
             if (p.gate) s[k] = sigmoid2(g[k]);
             m[k] = p.gate ? mul2(y[k], mul2(g[k], s[k])) : y[k];
         }
+        // The sums of both norms that do not need each other go together, with one barrier; (g unit) is
+        // (g v) / spread, so that the first norm's gradient does not wait for its spread.
+        if (p.center) {
+            const float4 means = sum.four(p.w_pre ? sum_all(u) : 0.f, p.w_post ? sum_all(m) : 0.f, 0.f, 0.f);
+            if (p.w_pre) shift_row<T, E>(u, means.x * p.inv_c, w);
+            if (p.w_post) shift_row<T, E>(m, means.y * p.inv_c, w);
+        }
+        f2 gw[H];
+        float suu = 0.f, sgu = 0.f, sg = 0.f;
+        if (p.w_pre) {
+            prm.get(kWPre, w, gw);
+#pragma unroll
+            for (int k = 0; k < H; ++k) gw[k] = mul2(go[k], gw[k]);
+            suu = dot_all(u, u);
+            sgu = dot_all(gw, u);
+            if (p.center) sg = sum_all(gw);
+        }
+        float4 sums = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (p.w_pre || p.w_post) sums = sum.four(suu, sgu, sg, p.w_post ? dot_all(m, m) : 0.f);
+        if (p.w_pre) {
+            const float rs = rsqrtf(fmaf(sums.x, p.inv_c, p.eps));
+#pragma unroll
+            for (int k = 0; k < H; ++k) u[k] = mul2(u[k], both(rs));
+            cols.template add<kDbPre>(p.slot[kDbPre], go);
+            cols.template add_product<kDwPre>(p.slot[kDwPre], go, u);
+            unit_back<H>(gw, u, rs, sums.y * rs, sums.z, p);
+#pragma unroll
+            for (int k = 0; k < H; ++k) d[k] = add2(d[k], gw[k]);
+        }
+        if (p.dr_in) st_row<T, R, E>((R*)p.dr_in + row * p.C, w, d);
         float rs = 1.f;
-        if (p.w_post) rs = to_unit<T, E, WARP>(m, p, w, sum);
+        if (p.w_post) {
+            rs = rsqrtf(fmaf(sums.w, p.inv_c, p.eps));
+#pragma unroll
+            for (int k = 0; k < H; ++k) m[k] = mul2(m[k], both(rs));
+        }
         if (p.slot[kDscale] >= 0) {
             f2 v[H];
 #pragma unroll
@@ -432,7 +475,9 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 && E == 8 ? 2 : 1) k_norm_bw
             cols.template add<kDbPost>(p.slot[kDbPost], d);
             cols.template add_product<kDwPost>(p.slot[kDwPost], d, m);
             scale_by<T, E>(d, prm, kWPost, w);
-            unit_back<H, WARP>(d, m, rs, p, sum);
+            const float a = dot_all(d, m);
+            const float2 back = p.center ? pair_of(sum.four(a, sum_all(d), 0.f, 0.f)) : make_float2(sum.one(a), 0.f);
+            unit_back<H>(d, m, rs, back.x, back.y, p);
         }
         if (p.gate) {
             if (p.dgate) {
