@@ -120,6 +120,10 @@ template <typename T, int P, bool WIDE, int S> struct Ring {
         n = channels;
         put = got = 0;
     }
+    // Waits for the copies of batches that nobody takes: before a thread ends, or fills their places anew.
+    __device__ __forceinline__ void leave() {
+        if constexpr (WIDE) asm volatile("cp.async.wait_all;" ::: "memory");
+    }
     // Takes the next batch (of the `tokens` that still come) and sends for the one S - 1 behind it. The
     // groups of several rings of a thread have to be issued in turn.
     template <int RINGS> __device__ __forceinline__ void take(R (&r)[kBatch], int tokens) {
@@ -240,7 +244,10 @@ __global__ void __launch_bounds__(128) k_conv_fwd(const ConvArgs p, long long bl
                     enter(p, s, t + u);
                     window<T, K, P>(p, xr, s, t + u, c, n, win);
                 }
-                if (p.cu && s.q >= p.S) return;                   // behind the last sequence
+                if (p.cu && s.q >= p.S) {                         // behind the last sequence
+                    ring.leave();
+                    return;
+                }
                 one(raw[u]);
             }
         }
@@ -417,6 +424,7 @@ __global__ void __launch_bounds__(128) k_conv_bwd(const ConvArgs p) {
                     shift();
                 }
             }
+            rx.leave();                                           // an early end leaves copies to places that the next run fills
             if (open && stop == s.end) {                          // ended with the sequence, inside the loop's last batch
 #pragma unroll
                 for (int k = 0; k < K - 1; ++k) put(stop - (K - 1) + k, acc[k]);
