@@ -28,16 +28,7 @@ struct ConvArgs {
     int nvec, run, runs;        // channel vectors; tokens of a run; runs of a row
 };
 
-// L consecutive elements (L * sizeof(T) = 8 or 16 bytes when wide), as floats.
-template <typename T, int L>
-__device__ __forceinline__ void ld_ch(const T* p, float (&v)[L], int n, bool wide) {
-    if (wide && n >= L) {
-        ld_lanes<T, L>(p, v);
-    } else {
-#pragma unroll
-        for (int i = 0; i < L; ++i) v[i] = i < n ? Io<T>::ld(p + i) : 0.f;
-    }
-}
+// L consecutive elements (L * sizeof(T) = 8 or 16 bytes when wide), from floats.
 template <typename T, int L>
 __device__ __forceinline__ void st_ch(T* p, const float (&v)[L], int n, bool wide) {
     if (wide && n >= L) {

@@ -836,7 +836,6 @@ Shape shape_for(int C) {
     if (n <= 4096) return {16, (n + 511) / 512 * 32, false, false};
     return {16, (C + 511) / 512 * 32, false, true};
 }
-constexpr size_t kSmem = 200 * 1024;
 // Shared memory: parameters, or the column sums of the backward pass of wide rows.
 size_t smem_for(const Shape& s, int slots) {
     if (s.wide) return (size_t)slots * 8 * s.threads * sizeof(f2);
@@ -862,7 +861,7 @@ cudaError_t by_shape(const NormArgs& p, int blocks, cudaStream_t st) {
     const size_t smem = smem_for(s, FWD ? 0 : p.slots);
     auto go = [&](auto kernel) {
         cudaError_t e = cudaSuccess;
-        if (smem > 48 * 1024) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (smem > 48 * 1024) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostSmem);
         if (e == cudaSuccess) kernel<<<blocks, s.threads, smem, st>>>(p);
         return e;
     };
@@ -970,7 +969,7 @@ gspn_status gspn_norm_backward(const gspn_norm_desc* desc, const void* y, const 
         if (outs[i]) to.to[p.slots++] = outs[i];
     }
     // the column sums of wide rows live in shared memory
-    if (p.C > kMaxC || smem_for(shape_for(p.C), p.slots) > kSmem) return GSPN_ERR_UNSUPPORTED;
+    if (p.C > kMaxC || smem_for(shape_for(p.C), p.slots) > 200 * 1024) return GSPN_ERR_UNSUPPORTED;
     if (ws_bytes < gspn_norm_workspace_size(desc, 1)) return GSPN_ERR_WORKSPACE;
     p.y = y; p.gate = gate; p.r = r_out; p.w_post = w_post; p.b_post = b_post; p.scale = scale; p.w_pre = w_pre;
     p.dr = dr; p.go = go; p.dy = dy; p.dr_in = dr_in; p.dgate = dgate;

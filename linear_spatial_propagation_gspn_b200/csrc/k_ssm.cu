@@ -1214,8 +1214,6 @@ __global__ void __launch_bounds__(kStep) k_ssm_step(const SsmArgs p, const int* 
 }
 
 // ---------------------------------------------------------------------------------------- host
-constexpr size_t kHalfSmem = 116 * 1024;
-
 // Two lanes for N <= 8 were no faster than four of which half idle (4 x 2048 x 4096: 324 us forward both).
 int lanes_for(int N) { return N <= 16 ? 4 : N <= 32 ? 8 : 16; }
 
@@ -1367,17 +1365,16 @@ gspn_status gspn_ssm_forward(const gspn_ssm_desc* desc, const void* x, const voi
         constexpr int NL = decltype(nl)::value;
         const unsigned cblocks = p.nb * p.G;
         auto go = [&](auto kernel, size_t smem, unsigned pieces) {
-            // Fewer blocks than SMs should have one SM each, but two of them fit on one and some would share it:
-            // ask for more shared memory than half of an SM's.
             const unsigned blocks = cblocks * pieces * p.S;
-            if (blocks <= (unsigned)device_sm_count() && smem < kHalfSmem) smem = kHalfSmem;
-            if (NL == 4) {
-                static const cudaError_t regs = check_registers(kernel, kFwdThreads4, kFwdRegs4);
-                if (e == cudaSuccess) e = regs;
-            }
-            if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+            if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostSmem);
             if (e == cudaSuccess) kernel<<<blocks, 32 * NL + Feed<NL>::threads, smem, st>>>(p);
         };
+        static_assert(sizeof(FwdSmem<T, NL, true>) <= kMostSmem && sizeof(FwdSmem<T, NL, false>) <= kMostSmem, "fits an SM");
+        if constexpr (NL == 4) {
+            static const cudaError_t first = check_registers(k_ssm_fwd<T, NL, true>, kFwdThreads4, kFwdRegs4);
+            static const cudaError_t main = check_registers(k_ssm_fwd<T, NL, false>, kFwdThreads4, kFwdRegs4);
+            e = first != cudaSuccess ? first : main;
+        }
         if (p.K > 1) go(k_ssm_fwd<T, NL, true>, sizeof(FwdSmem<T, NL, true>), p.K - 1);
         go(k_ssm_fwd<T, NL, false>, sizeof(FwdSmem<T, NL, false>), p.K);
     });
@@ -1422,10 +1419,11 @@ gspn_status gspn_ssm_backward(const gspn_ssm_desc* desc, const void* x, const vo
         constexpr int NL = decltype(nl)::value;
         const unsigned cblocks = p.nb * p.G;
         const size_t smem = sizeof(BwdSmem<T, NL>);
+        static_assert(sizeof(BwdSmem<T, NL>) <= kMostSmem, "fits an SM");
         static const cudaError_t regs = check_registers(k_ssm_bwd<T, NL>, kScan + kFeedB, kScan * kScanRegs + kFeedB * kFeedRegs);
         e = regs;
         if (e != cudaSuccess) return;
-        e = cudaFuncSetAttribute(k_ssm_bwd<T, NL>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        e = cudaFuncSetAttribute(k_ssm_bwd<T, NL>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostSmem);
         if (e != cudaSuccess) return;
         if (p.K > 1) k_ssm_bwd_local<T, NL><<<cblocks * (p.K - 1) * p.S, 32 * NL, 0, st>>>(p);
         k_ssm_bwd<T, NL><<<(unsigned)(p.nbb * p.G) * p.K * p.S, kScan + kFeedB, smem, st>>>(p);

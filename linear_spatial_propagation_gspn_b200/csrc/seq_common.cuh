@@ -49,18 +49,6 @@ __device__ __forceinline__ void unpack_raw(const uint4& q, float (&v)[Vec<T>::V]
     }
 }
 
-template <typename T>
-__device__ __forceinline__ void st_vec(T* p, const float (&v)[Vec<T>::V], int n, bool wide) {
-    constexpr int V = Vec<T>::V;
-    if (wide && n >= V) {
-        st_lanes<T, V>(p, v);
-    } else {
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-            if (i < n) Io<T>::st(p + i, v[i]);
-    }
-}
-
 // Four consecutive elements, as stored.
 template <typename T> struct Quad;
 template <> struct Quad<float> { typedef uint4 raw; };
@@ -97,6 +85,10 @@ __device__ __forceinline__ float ex2(float v) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
     return r;
 }
+
+// Dynamic shared memory that kernels over 48 KB are allowed: the same for every call, since calls at once would
+// set each other's limit.
+constexpr int kMostSmem = 224 * 1024;
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
