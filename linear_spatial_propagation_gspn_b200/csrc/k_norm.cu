@@ -2,9 +2,15 @@
 //   m = y silu(gate);  v = norm(m) w_post + b_post;  r_out = r + scale v;  o = norm(r_out) w_pre + b_pre
 // with norm(v) = v / sqrt(mean(v^2) + eps), of v - mean(v) when centred.
 //
-// Some tens of operations per element: memory traffic bounds it. A row stays in the registers of one
-// warp (narrow rows) or one block from its load to its last store, so every tensor crosses HBM once. Means are taken before squares of differences, from registers, so that
-// no cancellation enters. Statistics and sums are fp32.
+// Some tens of operations per element: memory traffic bounds the forward pass, and the backward one
+// about as much the instructions of its four sums over a row and the waits between them. A row stays in the
+// registers of one warp (narrow rows) or one block from its load to its last store, so every tensor crosses
+// HBM once. Means are taken before squares of differences, from registers, so that no cancellation enters.
+// Statistics and sums are fp32.
+//
+// Measured (B200): forward 8192 x 4096, bf16 with an fp32 stream, gate and both norms, 82 us, 5.7 TB/s;
+// backward 193 us, 3.8 TB/s. 8190 x 1153, bf16, centred, all parts: 40 us forward (2.4 TB/s), 77 us backward
+// (2.0 TB/s), 37 and 72 us at 1152 columns.
 #include "seq_common.cuh"
 
 namespace gspn {
@@ -31,8 +37,9 @@ struct NormArgs {
 
 // ---------------------------------------------------------------------------- rows of up to 4096
 // How a row is held. E elements (8; 16 over 2048 columns, so that no block has over eight warps to sum
-// over) in each thread of a block of as many warps as the row needs, or of one warp where 32 E cover it: V consecutive columns (16 bytes) at a time, E / V times over, as E / 2
-// pairs. Rows of an odd number of columns start at other distances from a 16-byte border: the columns
+// over: from 1024 columns on, 8190 x 1153 backward took 113 us against 77) in each thread of a block of as many
+// warps as the row needs, or of one warp where 32 E cover it: V consecutive columns (16 bytes) at a time,
+// E / V times over, as E / 2 pairs. Rows of an odd number of columns start at other distances from a 16-byte border: the columns
 // of a thread are shifted by that phase, so that every full vector is still one aligned load. A block
 // takes rows of one phase only (the grid is a multiple of the phases' period), so a thread keeps its
 // columns, and with them its parameters and column sums. Vectors that cross an end of the row, and all
@@ -359,22 +366,39 @@ __device__ __forceinline__ void unit_back(f2 (&g)[H], const f2 (&unit)[H], float
 
 __device__ __forceinline__ float2 pair_of(float4 v) { return make_float2(v.x, v.y); }
 
-// Column sums over the rows of a block, in registers: a thread's columns are its own.
-template <int H> struct Cols {
-    f2 v[kSums * H];
-    __device__ __forceinline__ void clear() {
-#pragma unroll
-        for (int i = 0; i < kSums * H; ++i) v[i] = both(0.f);
+// Column sums over the rows of a block, in shared memory: a thread's columns are its own, and a sum is touched
+// once a row. In registers they made the compiler spill (8190 x 1153 backward 93 us, so 77; 8192 x 4096 247 and
+// 193); with room for a fourth block of 96 or 112 registers it spilled again (93 and 81 us).
+template <int E> struct Cols {
+    float* at;                   // [sum][E / 4][thread][4]
+    __device__ __forceinline__ ulonglong2& place(int slot, int e) {
+        return *(ulonglong2*)(at + ((slot * (E / 4) + e / 4) * (int)blockDim.x + (int)threadIdx.x) * 4);
     }
-    template <int WHICH> __device__ __forceinline__ void add(int slot, const f2 (&x)[H]) {
+    __device__ __forceinline__ void clear(int slots) {
+        for (int i = 0; i < slots; ++i)
+#pragma unroll
+            for (int e = 0; e < E; e += 4) place(i, e) = make_ulonglong2(both(0.f), both(0.f));
+    }
+    __device__ __forceinline__ void add(int slot, const f2 (&x)[E / 2]) {
         if (slot < 0) return;
 #pragma unroll
-        for (int k = 0; k < H; ++k) v[WHICH * H + k] = add2(v[WHICH * H + k], x[k]);
+        for (int e = 0; e < E; e += 4) {
+            ulonglong2& s = place(slot, e);
+            const ulonglong2 v = s;
+            s = make_ulonglong2(add2(v.x, x[e / 2]), add2(v.y, x[e / 2 + 1]));
+        }
     }
-    template <int WHICH> __device__ __forceinline__ void add_product(int slot, const f2 (&x)[H], const f2 (&y)[H]) {
+    __device__ __forceinline__ void add_product(int slot, const f2 (&x)[E / 2], const f2 (&y)[E / 2]) {
         if (slot < 0) return;
 #pragma unroll
-        for (int k = 0; k < H; ++k) v[WHICH * H + k] = fma2(x[k], y[k], v[WHICH * H + k]);
+        for (int e = 0; e < E; e += 4) {
+            ulonglong2& s = place(slot, e);
+            const ulonglong2 v = s;
+            s = make_ulonglong2(fma2(x[e / 2], y[e / 2], v.x), fma2(x[e / 2 + 1], y[e / 2 + 1], v.y));
+        }
+    }
+    __device__ __forceinline__ float one(int slot, int thread, int e) const {
+        return at[((slot * (E / 4) + e / 4) * (int)blockDim.x + thread) * 4 + e % 4];
     }
 };
 
@@ -390,8 +414,8 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 && E == 8 ? 2 : 1) k_norm_bw
     long long row, step;
     const Row w = place<T, E, WARP>(p, row, step);
     const Params<T, E> prm = params<T, E, WARP>(p, w, smem, buf);
-    Cols<H> cols;
-    cols.clear();
+    Cols<E> cols{smem + kParams * E * blockDim.x};
+    cols.clear(p.slots);
     RowRaw<T, T, E> ny{}, ng{}, no{};
     RowRaw<T, R, E> nu{}, nd{};
     auto load = [&](long long r) {
@@ -450,8 +474,8 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 && E == 8 ? 2 : 1) k_norm_bw
             const float rs = rsqrtf(fmaf(sums.x, p.inv_c, p.eps));
 #pragma unroll
             for (int k = 0; k < H; ++k) u[k] = mul2(u[k], both(rs));
-            cols.template add<kDbPre>(p.slot[kDbPre], go);
-            cols.template add_product<kDwPre>(p.slot[kDwPre], go, u);
+            cols.add(p.slot[kDbPre], go);
+            cols.add_product(p.slot[kDwPre], go, u);
             unit_back<H>(gw, u, rs, sums.y * rs, sums.z, p);
 #pragma unroll
             for (int k = 0; k < H; ++k) d[k] = add2(d[k], gw[k]);
@@ -468,12 +492,12 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 && E == 8 ? 2 : 1) k_norm_bw
 #pragma unroll
             for (int k = 0; k < H; ++k) v[k] = m[k];
             if (p.w_post) scale_shift<T, E>(v, prm, kWPost, p.b_post != nullptr, w);
-            cols.template add_product<kDscale>(p.slot[kDscale], v, d);
+            cols.add_product(p.slot[kDscale], v, d);
         }
         if (p.scale) scale_by<T, E>(d, prm, kScale, w);
         if (p.w_post) {
-            cols.template add<kDbPost>(p.slot[kDbPost], d);
-            cols.template add_product<kDwPost>(p.slot[kDwPost], d, m);
+            cols.add(p.slot[kDbPost], d);
+            cols.add_product(p.slot[kDwPost], d, m);
             scale_by<T, E>(d, prm, kWPost, w);
             const float a = dot_all(d, m);
             const float2 back = p.center ? pair_of(sum.four(a, sum_all(d), 0.f, 0.f)) : make_float2(sum.one(a), 0.f);
@@ -495,33 +519,26 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 && E == 8 ? 2 : 1) k_norm_bw
     // this block's sums: [sum][C]
     float* part = p.part + (long long)blockIdx.x * p.slots * p.C;
     if constexpr (WARP) {
-        // the four warps' sums in order, one sum at a time through shared memory
-        float (*red)[32 * E] = (float(*)[32 * E])smem;
+        // rows of the four warps are shifted by their own phases: a column's sums lie in four places
+        __syncthreads();
+        for (int i = 0; i < p.slots; ++i)
+            for (int c = threadIdx.x; c < p.C; c += blockDim.x) {
+                float v[4];
 #pragma unroll
-        for (int i = 0; i < kSums; ++i) {
-            if (p.slot[i] < 0) continue;
-            __syncthreads();
-#pragma unroll
-            for (int e = 0; e < E; ++e) {
-                const float2 f = unpack(cols.v[i * H + e / 2]);
-                const int c = Y::col(w, e);
-                if (c >= 0 && c < p.C) red[threadIdx.x >> 5][c] = e & 1 ? f.y : f.x;
+                for (int k = 0; k < 4; ++k) {
+                    const long long first = (long long)blockIdx.x * 4 + k;
+                    const int at = c + (w.wide ? (int)(first * p.C % Y::V) : 0), vec = at / Y::V;
+                    v[k] = cols.one(i, k * 32 + vec % 32, vec / 32 * Y::V + at % Y::V);
+                }
+                part[i * p.C + c] = (v[0] + v[1]) + (v[2] + v[3]);
             }
-            __syncthreads();
-            for (int c = threadIdx.x; c < p.C; c += blockDim.x)
-                part[p.slot[i] * p.C + c] = (red[0][c] + red[1][c]) + (red[2][c] + red[3][c]);
-        }
     } else {
-#pragma unroll
-        for (int i = 0; i < kSums; ++i) {
-            if (p.slot[i] < 0) continue;
+        for (int i = 0; i < p.slots; ++i)
 #pragma unroll
             for (int e = 0; e < E; ++e) {
                 const int c = Y::col(w, e);
-                const float2 f = unpack(cols.v[i * H + e / 2]);
-                if (c >= 0 && c < p.C) part[p.slot[i] * p.C + c] = e & 1 ? f.y : f.x;
+                if (c >= 0 && c < p.C) part[i * p.C + c] = cols.one(i, threadIdx.x, e);
             }
-        }
     }
 }
 
@@ -823,8 +840,8 @@ bool make_args(const gspn_norm_desc* d, NormArgs* p) {
     return true;
 }
 
-// How a row is held: elements of a thread, threads of a block (128 = four warps with a row each, `warp`), up to seven places
-// kept free for the phase; `wide`: the kernels for wide rows.
+// How a row is held: elements of a thread, threads of a block (128 = four warps with a row each, `warp`), up to
+// seven places kept free for the phase; `wide`: the kernels for wide rows.
 struct Shape {
     int e, threads;
     bool warp, wide;
@@ -836,10 +853,10 @@ Shape shape_for(int C) {
     if (n <= 4096) return {16, (n + 511) / 512 * 32, false, false};
     return {16, (C + 511) / 512 * 32, false, true};
 }
-// Shared memory: parameters, or the column sums of the backward pass of wide rows.
+// Shared memory: parameters and the backward pass's column sums; of wide rows the latter only.
 size_t smem_for(const Shape& s, int slots) {
     if (s.wide) return (size_t)slots * 8 * s.threads * sizeof(f2);
-    return (size_t)s.threads * s.e * kParams * sizeof(float);
+    return (size_t)s.threads * s.e * (kParams + slots) * sizeof(float);
 }
 // Blocks: what fits the SMs at once by their registers (threads an SM: backward 512, 256 with 16 elements;
 // forward twice that), in whole periods of the phases, and no more than there are rows. Wide rows have
@@ -848,7 +865,7 @@ int blocks_for(const gspn_norm_desc& d, bool bwd) {
     const Shape s = shape_for(d.C);
     const long long groups = s.warp ? ((long long)d.rows + 3) / 4 : d.rows;
     if (s.wide && !bwd) return d.rows;
-    const int fill = (s.e == 8 ? 512 : 256) * (bwd ? 1 : 2);
+    const int fill = bwd ? (s.e == 8 ? 512 : 256) : s.e == 8 ? 1024 : 512;
     long long n = (long long)device_sm_count() * (s.threads >= fill ? 1 : fill / s.threads);
     n = n / 8 * 8;
     n = groups < n ? groups : n;
