@@ -16,6 +16,8 @@
  *     weights, scale), scan states and parameter gradients are fp32 for both. Arithmetic is fp32
  *     and each output is rounded once.
  *   - L and rows may be 0. Every other size is at least 1.
+ *   - Outputs overlap neither inputs nor each other, except where a call says so.
+ *   - B * L < 2^31 and L <= 2^30; beyond what a launch can count, GSPN_ERR_UNSUPPORTED.
  *   - Pointers must be aligned to their element; 16-byte aligned rows take the wide loads. The
  *     workspace must be 16-byte aligned. A call whose workspace size is 256 needs none of it and
  *     takes a null workspace.
@@ -60,7 +62,7 @@ GSPN_API gspn_status gspn_conv_backward(const gspn_conv_desc *desc, const void *
 /* One token for each of desc->B rows (desc->L = 1, x_tok unused): y B x C; state: slots x K-1 x C,
  * updated in place. idx (device, B ints, or null: row b has slot b) names each row's slot; a row
  * whose index is outside [0, slots) is skipped and its y left as it was. Rows that name one slot
- * take their tokens in row order. */
+ * take their tokens in row order. At most 65535 rows. */
 GSPN_API gspn_status gspn_conv_step(const gspn_conv_desc *desc, const void *x, const float *w, const float *bias,
                                     const int *idx, int slots, void *state, void *y, void *stream);
 
@@ -103,7 +105,7 @@ GSPN_API gspn_status gspn_ssm_backward(const gspn_ssm_desc *desc, const void *x,
                                        size_t ws_bytes, void *stream);
 
 /* One token for each of desc->B rows (desc->L = 1, *_tok unused): y B x C; h: slots x C x N, updated
- * in place; idx and slots as for gspn_conv_step. */
+ * in place; idx and slots as for gspn_conv_step. C * N < 2^30. */
 GSPN_API gspn_status gspn_ssm_step(const gspn_ssm_desc *desc, const void *x, const void *dt, const float *A,
                                    const void *Bm, const void *Cm, const float *D, const void *z,
                                    const float *dt_bias, const int *idx, int slots, float *h, void *y,
@@ -115,7 +117,7 @@ GSPN_API gspn_status gspn_ssm_step(const gspn_ssm_desc *desc, const void *x, con
  * center = 1. Left out where the pointer is null: gate; the norm behind the block (w_post); r;
  * scale; the norm before the next block (w_pre, then o is null too). b_post and b_pre need their
  * weight. r and r_out are of res_dtype: GSPN_F32, or dtype. o is computed from r_out before it is
- * rounded. C <= 16384. */
+ * rounded; r_out may be r itself (with r_row = C). C <= 16384. */
 typedef struct {
     int rows, C;
     int dtype;               /* gspn_dtype of y, gate, o */
@@ -135,7 +137,9 @@ GSPN_API gspn_status gspn_norm_forward(const gspn_norm_desc *desc, const void *y
 /* Gradients of sum(dr r_out) + sum(go o), given r_out as the forward left it (r_row is its row
  * stride): dy, dr_in (the gradient of r, res_dtype), dgate, dw_post, db_post, dscale, dw_pre, db_pre.
  * dr (or null), go: rows x C contiguous, dr of res_dtype. go and r_out go with w_pre. Each output
- * may be null where its input is null; dr_in may be null. */
+ * may be null where its input is null; dr_in may be null. Rows over 4096 columns have their column sums in
+ * shared memory: asked for more than 200 KB of them, the call returns GSPN_ERR_UNSUPPORTED (all five
+ * fit up to 10240 columns, four up to 12800, three up to 16384). */
 GSPN_API gspn_status gspn_norm_backward(const gspn_norm_desc *desc, const void *y, const void *gate,
                                         const float *w_post, const float *b_post, const float *scale,
                                         const void *r_out, const float *w_pre, const void *dr, const void *go,

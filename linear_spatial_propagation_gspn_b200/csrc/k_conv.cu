@@ -1,10 +1,14 @@
 // k_conv.cu -- short causal convolution over token sequences, one filter of K taps per channel:
 //   u_t = bias + sum_{k<K} w_k x_{t-K+1+k},   y_t = u_t or u_t sigmoid(u_t).
 //
-// A few operations per element, so memory traffic bounds it: x read and y written once. A thread
-// keeps four channels (eight of bf16 took registers that more warps use better) and walks a run of tokens with the K - 1 inputs
-// before the present one in registers, so each input is loaded once per run; the K - 1 tokens that
-// neighbouring runs share come from the caches.
+// A few operations per element, so memory traffic should bound it: x read and y written once. A thread
+// keeps four channels (eight of bf16 took registers that more warps use better) and walks a run of tokens
+// with the K - 1 inputs before the present one in registers, so each input is loaded once per run; the
+// K - 1 tokens that neighbouring runs share come from the caches.
+//
+// Measured (B200, bf16, K = 4, silu): forward 8192 x 4096 33 us, 4.1 TB/s; 4 x 2048 x 2048 20 us, 3.3 TB/s;
+// backward of the latter 36 us, 2.8 TB/s, and 4.5 us for the sums of dw. A silu and its slope cost about as
+// many instruction slots (45 % taken) as the traffic costs time.
 #include "seq_common.cuh"
 
 namespace gspn {

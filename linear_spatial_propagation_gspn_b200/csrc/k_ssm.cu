@@ -8,15 +8,21 @@
 //
 // Layout of a block: 32 channels of one sequence (64 bytes of a bf16 row: whole sectors) and
 // NL = ceil(N / 4) rounded up to 4, 8 or 16 lanes for each channel, four states in registers per
-// lane. Tokens come in tiles of 32: each thread loads its part of the next tile into registers
-// while the present one is scanned from shared memory, where the steps d and d x are formed once
-// per (t, c). Sums over n stay in the NL lanes of a channel: four tokens at a time are reduced and
-// scattered, so that each lane ends with one token's sum.
+// lane. Some warps scan tiles of tokens from shared memory; others load the next tile, form the steps
+// d and d x once per (t, c), add the lanes' shares of the sums over n and write y.
 //
 // Parallel over channels and sequences alone, a block walks its whole sequence. Where that leaves
 // most of the chip idle, every sequence is cut into K equal pieces: a first pass finds each piece's
 // own state from zero and its sum of steps (the decay over the piece is exp(A sum d)), and the main
 // pass joins the pieces before its own. That makes every exponential twice.
+//
+// Measured (B200, bf16, N = 16, gate, D and bias), against the exponentials' time alone:
+//   forward, 4 x 2048 tokens of 2048 channels, states saved   160 us   59 us   (two blocks an SM: 68 % of issue slots)
+//   the same backward                                         437 us   59 us   (54 % of issue slots, one block an SM)
+//   forward, one sequence of 16384 tokens, 4096 channels      686 us  236 us   (128 blocks, 81 cycles a token)
+//   a token of 256 rows of 4096 channels                       34 us   4.2 TB/s of states, A and inputs
+// Issue slots and, with one block an SM, the scanning warp's latencies stand before the exponentials: a
+// token costs a block 200 instructions forward, of which the four scanning warps take about half.
 #include "seq_common.cuh"
 
 namespace gspn {
@@ -191,9 +197,10 @@ __device__ __forceinline__ void ld_states(T (&r)[E], const void* base, long long
 }
 
 // ------------------------------------------------------------------------------------- forward
-// The block's first NL warps scan; eight more (four for NL = 16) feed them: they load the tokens, form d and d x, and turn
-// the sums over n of the tile before into y. The two work on neighbouring tiles, with one barrier a
-// tile, so the long latencies of the one side hide behind the other's arithmetic.
+// The block's first NL warps scan; eight more (four for NL = 16) feed them: they load the tokens, form d and d x,
+// and turn the sums over n of the tile before into y. The two work on neighbouring tiles, with one barrier a
+// tile, so the long latencies of the one side hide behind the other's arithmetic (16384 x 4096: 1866 us with
+// every warp doing both, 817 with four feeding warps, 690 with eight).
 // A token's shares of the sums over n, NL for each channel, with four floats between the vectors of
 // channels that one feeding thread adds up: its neighbours then start on other banks.
 template <int NL> struct YRow {
@@ -477,7 +484,8 @@ __global__ void __launch_bounds__(32 * NL + Feed<NL>::threads, NL == 4 ? 2 : 1) 
 // two. Those sums go over the warp's channel lanes by halving: what one lane gives away is what its
 // partner keeps. No selects are needed, since a lane holds its states in an order of its own (slot j is
 // state j xor the lane's low bits). The sums over n go the same way once (the two channels of
-// neighbouring lanes are in opposite order), and the feeding warps add the rest.
+// neighbouring lanes are in opposite order), and the feeding warps add the rest. One channel a lane and
+// eight scanning warps took 557 cycles a token of 64 channels against 464.
 constexpr int perm_copies(int NL) { return 32 / NL < 4 ? 32 / NL : 4; }
 
 __device__ __forceinline__ void permute4(float (&v)[4], int pm) {
@@ -1454,11 +1462,14 @@ gspn_status gspn_ssm_step(const gspn_ssm_desc* desc, const void* x, const void* 
     p.x = x; p.dt = dt; p.z = z; p.Bm = Bm; p.Cm = Cm; p.A = A; p.D = D; p.bias = dt_bias; p.h = h; p.y = y;
     p.wide = p.N % 4 == 0 && aligned_to(h, 16) && aligned_to(A, 16);
     p.wide_bc = p.N % 4 == 0 && wide_ok(Bm, p.b_row, 0, es) && wide_ok(Cm, p.c_row, 0, es);
-    // Four channels a lane where that leaves four blocks for each SM; rows share a block (and its reading
-    // of A) as far as eight remain.
+    // Four channels a lane in the plain form (against one: a row of 4096 channels 2.2 us either way, 12 rows 4.8 and
+    // 6.2 us, 256 rows 34 and 43); in the general form only where that leaves four blocks for each SM (2000 channels
+    // of 24 states: 4 rows 4.3 and 3.2 us, 32 rows 8.7 and 9.8, 256 rows 52 and 61). Rows share a block (and
+    // its reading of A) as far as eight remain.
     const int NL = lanes_for(p.N);
     const long long sms = device_sm_count(), wide_blocks = (p.C + 4 * kStep / NL - 1) / (4 * kStep / NL);
-    const bool four = wide_blocks * p.B >= 4 * sms;
+    const bool plain = p.G == 1 && p.N == 4 * NL && p.wide && p.wide_bc && p.C % (4 * kStep / NL) == 0;
+    const bool four = plain || wide_blocks * p.B >= 4 * sms;
     const long long gx = four ? wide_blocks : (p.C + kStep / NL - 1) / (kStep / NL);
     long long group = gx * p.B / (8 * sms);
     group = group < 1 ? 1 : group > kGroup ? kGroup : group;
@@ -1468,9 +1479,9 @@ gspn_status gspn_ssm_step(const gspn_ssm_desc* desc, const void* x, const void* 
         using T = decltype(t);
         constexpr int N = decltype(nl)::value;
         auto go = [&](auto kernel) { kernel<<<grid, kStep, 0, st>>>(p, idx, slots, (int)group); };
-        const bool plain = p.G == 1 && p.N == 4 * N && p.wide && p.wide_bc && p.C % ((four ? 4 : 1) * kStep / N) == 0;
-        if (four) plain ? go(k_ssm_step<T, N, 4, true>) : go(k_ssm_step<T, N, 4, false>);
-        else plain ? go(k_ssm_step<T, N, 1, true>) : go(k_ssm_step<T, N, 1, false>);
+        if (plain) go(k_ssm_step<T, N, 4, true>);
+        else if (four) go(k_ssm_step<T, N, 4, false>);
+        else go(k_ssm_step<T, N, 1, false>);
     });
     return last_status();
 }

@@ -145,6 +145,18 @@ def test_leading_axes_and_slices():
         R.check(r_out.view(6, 96), ref["r_out"], b, 1.0, f"rows of {width} from {at}")
 
 
+@pytest.mark.parametrize("C", [96, 257, 1153, 2048, 4096, 5000])
+@pytest.mark.parametrize("types", [("f32", "f32"), ("bf16", "bf16"), ("bf16", "f32")])
+def test_stream_in_place(C, types):
+    t = make(700, C, *types, seed=5)
+    kw = {k: t[k] for k in PARTS["all"]}
+    want = g.norm_forward(t["y"], t["r"], center=True, **kw)
+    r = t["r"].clone()
+    got = g.norm_forward(t["y"], r, center=True, r_out=r, **kw)
+    assert got[0] is r or got[0].data_ptr() == r.data_ptr()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
 def test_one_bad_row_stays_alone():
     t = make(9, 192, "f32", "f32")
     kw = {k: t[k] for k in PARTS["all"]}
