@@ -1041,11 +1041,13 @@ __global__ void k_ssm_sum_ac(const float* dA_part, const float* dch_part, int sl
     if (i < na) {
         const int n = (int)(i % Np);
         float w = 0.f;
+#pragma unroll 8
         for (int k = 0; k < slots; ++k) w += dA_part[k * na + i];
         if (n < N) dA[i / Np * N + n] = w;
     } else if (i < na + 2 * C) {
         const long long c = i - na;
         float w = 0.f;
+#pragma unroll 8
         for (int k = 0; k < slots; ++k) w += dch_part[(long long)k * 2 * C + c];
         float* out = c < C ? dD : dbias;
         if (out) out[c % C] = w;
@@ -1252,19 +1254,34 @@ bool fits(const SsmArgs& p) {
            (long long)p.S * p.nb * p.G * 64 < (1LL << 31);
 }
 
-// Pieces of a sequence. A block that has an SM to itself takes 81 cycles a token, two that share it 132,
-// and the first pass over pieces costs 0.6 of the main one (bf16, N = 16), so pieces pay where whole
-// sequences fill less than 3/4 of the SMs. Then as many as fit two to an SM at once, of 64 tokens at
-// least.
-int pieces_for(const SsmArgs& p, int sms) {
-    const long long blocks = (long long)p.S * p.nb * p.G;
+// Pieces of a sequence: as many (32 at most, of 64 tokens at least) as make the call shortest by this
+// account, in units of one block's walk over a whole sequence. Blocks run in waves of one for each SM; two
+// forward blocks of up to 16 states fit one and then take 1.63 times as long (132 cycles a token, not 81). The
+// first pass over pieces costs 0.6 of the main one forward; backward a third, without waves, since its
+// blocks are small; joining them takes about 24 tokens' time for each piece, backward 12. Measured at 4096 tokens, bf16, N = 16 (us whole, then for these numbers of pieces):
+//   forward    64 blocks 178, 4: 144, 10: 135    80 blocks 177, 3: 184, 10: 161   100 blocks 180, 2: 223, 8: 194
+//   backward   10 blocks 779, 6: 220, 12: 141    32 blocks 787, 4: 349, 12: 304    50 blocks 798, 2: 598, 8: 439
+// Forward a larger number has to gain 3 %, since the account is no better than that.
+int pieces_for(const SsmArgs& p, bool bwd, int sms) {
+    const long long blocks = (long long)p.S * p.G * (bwd ? p.nbb : p.nb);
     const long long len = p.S > 0 && p.cu ? p.L / p.S : p.L;
-    if (4 * blocks >= 3LL * sms) return 1;
-    long long K = 2LL * sms / blocks;
-    K = K < 64 ? K : 64;
-    const long long most = len / 64;
-    K = K < most ? K : most;
-    return K < 2 ? 1 : (int)K;
+    if (blocks >= sms || len < 128) return 1;
+    const bool pairs = !bwd && p.N <= 16;
+    auto waves = [&](long long n) {
+        if (!pairs) return (double)((n + sms - 1) / sms);
+        const long long rest = n % (2 * sms);
+        return n / (2 * sms) * 1.63 + (rest == 0 ? 0.0 : rest <= sms ? 1.0 : 1.63);
+    };
+    const int most = (int)(len / 64 < 32 ? len / 64 : 32);
+    int best = 1;
+    double least = 0.97;
+    for (int K = 2; K <= most; ++K) {
+        const double all = (double)(K - 1) * blocks / sms;
+        const double first = bwd ? 0.33 * (all > 1.0 ? all : 1.0) : 0.6 * waves((K - 1) * blocks);
+        const double cost = (waves(K * blocks) + first) / K + (bwd ? 12.0 : 24.0) * K / len;
+        if (cost < (bwd ? 0.995 : 0.97) * least) least = cost, best = K;
+    }
+    return best;
 }
 
 // The warps that scan take over registers of the ones that feed (setmaxnreg): the two shares have to be
@@ -1329,7 +1346,7 @@ size_t gspn_ssm_workspace_size(const gspn_ssm_desc* desc, int for_backward) {
     SsmArgs p;
     if (!make_args(desc, &p) || !fits(p)) return 0;
     p.cu = desc->S > 0 ? (const int*)8 : nullptr;
-    p.K = pieces_for(p, device_sm_count());
+    p.K = pieces_for(p, for_backward != 0, device_sm_count());
     return carve(p, for_backward != 0).total;
 }
 
@@ -1358,7 +1375,7 @@ gspn_status gspn_ssm_forward(const gspn_ssm_desc* desc, const void* x, const voi
     if (!aligned_to(hsave, 16) || !aligned_to(ws, 16)) return GSPN_ERR_ALIGNMENT;
     p.x = x; p.dt = dt; p.z = z; p.Bm = Bm; p.Cm = Cm; p.A = A; p.D = D; p.bias = dt_bias; p.cu = cu; p.h0 = h0;
     p.y = y; p.h = h; p.hsave = hsave;
-    p.K = pieces_for(p, device_sm_count());
+    p.K = pieces_for(p, false, device_sm_count());
     const Carve w = carve(p, false);
     if (p.K > 1 && !ws) return GSPN_ERR_INVALID_ARG;
     if (p.K > 1 && ws_bytes < w.total) return GSPN_ERR_WORKSPACE;
@@ -1411,7 +1428,7 @@ gspn_status gspn_ssm_backward(const gspn_ssm_desc* desc, const void* x, const vo
     if (!aligned_to(hsave, 16) || !aligned_to(ws, 16)) return GSPN_ERR_ALIGNMENT;
     p.x = x; p.dt = dt; p.z = z; p.Bm = Bm; p.Cm = Cm; p.A = A; p.D = D; p.bias = dt_bias; p.cu = cu;
     p.hsave = const_cast<float*>(hsave); p.dy = dy; p.dh = dh; p.dx = dx; p.ddt = ddt; p.dz = dz; p.dh0 = dh0;
-    p.K = pieces_for(p, device_sm_count());
+    p.K = pieces_for(p, true, device_sm_count());
     const Carve w = carve(p, true);
     if (ws_bytes < w.total) return GSPN_ERR_WORKSPACE;
     auto at = [&](size_t off) { return (float*)((char*)ws + off); };
