@@ -43,6 +43,25 @@ struct {
 #define NEED(c) \
     if (!(c)) DECLINE
 
+// A call that got as far as the device must not be made again by the Python path: a step would move its
+// states twice. Its error is raised here.
+PyObject* raised(const char* what, int status) {
+    PyObject* package = PyImport_ImportModule("linear_spatial_propagation_gspn_b200");
+    PyObject* type = package ? PyObject_GetAttrString(package, "GspnError") : nullptr;
+    PyObject* error = type ? PyObject_CallFunction(type, "is", status, what) : nullptr;
+    if (error) PyErr_SetObject(type, error);
+    Py_XDECREF(error);
+    Py_XDECREF(type);
+    Py_XDECREF(package);
+    return nullptr;
+}
+#define RUN(name, ...)                                             \
+    {                                                              \
+        const int status = lib.name(__VA_ARGS__);                  \
+        if (status == GSPN_ERR_CUDA) return raised("gspn_" #name, status); \
+        NEED(status == GSPN_OK);                                   \
+    }
+
 typedef const Tensor* Opt;
 
 // A plain tensor (or Parameter), or None.
@@ -60,6 +79,8 @@ bool all(PyObject* const* a, std::initializer_list<Opt*> to) {
         if (!get(*a++, *t)) return false;
     return true;
 }
+
+bool yes(PyObject* o) { return o == Py_True; }
 
 // The call's device and storage type.
 struct Ctx {
@@ -164,12 +185,12 @@ PyObject* conv_forward(PyObject*, PyObject* const* a, Py_ssize_t) {
     NEED(c.start(x));
     gspn_conv_desc d;
     int64_t n;
-    NEED(conv_desc(c, x, w, bias, PyObject_IsTrue(a[7]), cu, d, n));
+    NEED(conv_desc(c, x, w, bias, yes(a[7]), cu, d, n));
     NEED(c.opt(state0, c.ty, {n, d.K - 1, d.C}) && c.opt(state, c.ty, {n, d.K - 1, d.C}));
     Out o;
     NEED(o.take(c, y, true, c.ty, x->sizes()));
-    NEED(lib.conv_forward(&d, ptr(x), as<float>(w), as<float>(bias), as<int>(cu), ptr(state0), ptr(o.t), ptr(state),
-                          c.stream()) == GSPN_OK);
+    RUN(conv_forward, &d, ptr(x), as<float>(w), as<float>(bias), as<int>(cu), ptr(state0), ptr(o.t), ptr(state),
+                          c.stream());
     return o.object(a[5]);
 }
 
@@ -181,7 +202,7 @@ PyObject* conv_backward(PyObject*, PyObject* const* a, Py_ssize_t) {
     NEED(c.start(x));
     gspn_conv_desc d;
     int64_t n;
-    NEED(conv_desc(c, x, w, bias, PyObject_IsTrue(a[7]), cu, d, n));
+    NEED(conv_desc(c, x, w, bias, yes(a[7]), cu, d, n));
     const int64_t ss[3] = {n, d.K - 1, d.C};
     NEED(c.is(dy, c.ty, x->sizes()) && c.opt(state0, c.ty, ss) && c.opt(dstate, c.ty, ss));
     const size_t bytes = lib.conv_ws(&d, 1);
@@ -190,9 +211,9 @@ PyObject* conv_backward(PyObject*, PyObject* const* a, Py_ssize_t) {
     Out dx, dw, db, ds;
     NEED(dx.take(c, nullptr, true, c.ty, x->sizes()) && dw.take(c, nullptr, true, ScalarType::Float, w->sizes()) &&
          db.take(c, nullptr, bias, ScalarType::Float, {d.C}) && ds.take(c, nullptr, state0, c.ty, ss));
-    NEED(lib.conv_backward(&d, ptr(x), as<float>(w), as<float>(bias), as<int>(cu), ptr(state0), ptr(dy), ptr(dstate),
+    RUN(conv_backward, &d, ptr(x), as<float>(w), as<float>(bias), as<int>(cu), ptr(state0), ptr(dy), ptr(dstate),
                            ptr(dx.t), as<float>(dw.t), as<float>(db.t), ptr(ds.t), ws.data_ptr(), bytes,
-                           c.stream()) == GSPN_OK);
+                           c.stream());
     return tuple({dx.object(nullptr), dw.object(nullptr), db.object(nullptr), ds.object(nullptr)});
 }
 
@@ -209,12 +230,12 @@ PyObject* conv_step(PyObject*, PyObject* const* a, Py_ssize_t) {
          fits_int(x->sizes()));
     const int64_t B = x->size(0), C = x->size(1), K = w->size(1);
     NEED(c.f32(w, {C, K}) && c.opt_f32(bias, {C}) && c.is(state, c.ty, {state->size(0), K - 1, C}) && slots_ok(c, idx, state, B));
-    gspn_conv_desc d{(int)B, 1, (int)C, (int)K, 0, c.code(), PyObject_IsTrue(a[6]), 0, 0};
+    gspn_conv_desc d{(int)B, 1, (int)C, (int)K, 0, c.code(), yes(a[6]), 0, 0};
     NEED(c.tokens(x, x->sizes(), 1, d.x_row, d.x_tok));
     Out o;
     NEED(o.take(c, y, true, c.ty, x->sizes()));
-    NEED(lib.conv_step(&d, ptr(x), as<float>(w), as<float>(bias), as<int>(idx), (int)state->size(0), ptr(state), ptr(o.t),
-                       c.stream()) == GSPN_OK);
+    RUN(conv_step, &d, ptr(x), as<float>(w), as<float>(bias), as<int>(idx), (int)state->size(0), ptr(state), ptr(o.t),
+                       c.stream());
     return o.object(a[5]);
 }
 
@@ -243,14 +264,14 @@ PyObject* ssm_forward(PyObject*, PyObject* const* a, Py_ssize_t) {
     Opt x, dt, A, B, C, D, z, bias, cu, h0, y, h;
     NEED(all(a, {&x, &dt, &A, &B, &C, &D, &z, &bias, &cu, &h0, &y, &h}));
     Ctx c;
-    NEED(c.start(x));
+    NEED(c.start(x) && PyBool_Check(a[12]));
     gspn_ssm_desc d;
     int64_t n;
-    NEED(ssm_desc(c, x, dt, A, B, C, D, z, bias, PyObject_IsTrue(a[12]), cu, d, n));
+    NEED(ssm_desc(c, x, dt, A, B, C, D, z, bias, yes(a[12]), cu, d, n));
     NEED(c.opt_f32(h0, {n, d.C, d.N}) && c.opt_f32(h, {n, d.C, d.N}));
     Out o;
     NEED(o.take(c, y, true, c.ty, x->sizes()));
-    const bool save = PyObject_IsTrue(a[13]);
+    const bool save = yes(a[13]);
     Tensor hsave, ws;
     if (save) {
         const size_t bytes = lib.ssm_hsave(&d);
@@ -260,9 +281,9 @@ PyObject* ssm_forward(PyObject*, PyObject* const* a, Py_ssize_t) {
     const size_t bytes = lib.ssm_ws(&d, 0);
     NEED(bytes > 0);
     if (bytes > 256) ws = c.empty({(int64_t)bytes}, ScalarType::Byte);
-    NEED(lib.ssm_forward(&d, ptr(x), ptr(dt), as<float>(A), ptr(B), ptr(C), as<float>(D), ptr(z), as<float>(bias), as<int>(cu),
+    RUN(ssm_forward, &d, ptr(x), ptr(dt), as<float>(A), ptr(B), ptr(C), as<float>(D), ptr(z), as<float>(bias), as<int>(cu),
                          as<float>(h0), ptr(o.t), as<float>(h), save ? (float*)hsave.data_ptr() : nullptr,
-                         bytes > 256 ? ws.data_ptr() : nullptr, bytes, c.stream()) == GSPN_OK);
+                         bytes > 256 ? ws.data_ptr() : nullptr, bytes, c.stream());
     if (!save) return o.object(a[10]);
     return tuple({o.object(a[10]), wrap(hsave)});
 }
@@ -275,7 +296,7 @@ PyObject* ssm_backward(PyObject*, PyObject* const* a, Py_ssize_t) {
     NEED(c.start(x));
     gspn_ssm_desc d;
     int64_t n;
-    NEED(ssm_desc(c, x, dt, A, B, C, D, z, bias, PyObject_IsTrue(a[13]), cu, d, n));
+    NEED(ssm_desc(c, x, dt, A, B, C, D, z, bias, yes(a[13]), cu, d, n));
     const int64_t ss[3] = {n, d.C, d.N};
     NEED(c.is(dy, c.ty, x->sizes()) && c.opt_f32(h0, ss) && c.opt_f32(dh, ss) &&
          c.f32(hsave, {(int64_t)lib.ssm_hsave(&d) / 4}));
@@ -288,10 +309,10 @@ PyObject* ssm_backward(PyObject*, PyObject* const* a, Py_ssize_t) {
          dA.take(c, nullptr, true, f, A->sizes()) && dB.take(c, nullptr, true, c.ty, B->sizes()) &&
          dC.take(c, nullptr, true, c.ty, B->sizes()) && dD.take(c, nullptr, D, f, {d.C}) &&
          dz.take(c, nullptr, z, c.ty, x->sizes()) && dbias.take(c, nullptr, bias, f, {d.C}) && dh0.take(c, nullptr, h0, f, ss));
-    NEED(lib.ssm_backward(&d, ptr(x), ptr(dt), as<float>(A), ptr(B), ptr(C), as<float>(D), ptr(z), as<float>(bias), as<int>(cu),
+    RUN(ssm_backward, &d, ptr(x), ptr(dt), as<float>(A), ptr(B), ptr(C), as<float>(D), ptr(z), as<float>(bias), as<int>(cu),
                           as<float>(hsave), ptr(dy), as<float>(dh), ptr(dx.t), ptr(ddt.t), as<float>(dA.t), ptr(dB.t), ptr(dC.t),
                           as<float>(dD.t), ptr(dz.t), as<float>(dbias.t), as<float>(dh0.t), ws.data_ptr(), bytes,
-                          c.stream()) == GSPN_OK);
+                          c.stream());
     return tuple({dx.object(nullptr), ddt.object(nullptr), dA.object(nullptr), dB.object(nullptr), dC.object(nullptr),
                   dD.object(nullptr), dz.object(nullptr), dbias.object(nullptr), dh0.object(nullptr)});
 }
@@ -313,15 +334,15 @@ PyObject* ssm_step(PyObject*, PyObject* const* a, Py_ssize_t) {
     d.G = (int)G;
     d.N = (int)N;
     d.dtype = c.code();
-    d.softplus = PyObject_IsTrue(a[11]);
+    d.softplus = yes(a[11]);
     long long none;
     NEED(c.tokens(x, x->sizes(), 1, d.x_row, none) && c.tokens(dt, x->sizes(), 1, d.dt_row, none) &&
          (!z || c.tokens(z, x->sizes(), 1, d.z_row, none)) && c.tokens(B, {R, G, N}, 1, d.b_row, none) &&
          c.tokens(C, {R, G, N}, 1, d.c_row, none));
     Out o;
     NEED(o.take(c, y, true, c.ty, x->sizes()));
-    NEED(lib.ssm_step(&d, ptr(x), ptr(dt), as<float>(A), ptr(B), ptr(C), as<float>(D), ptr(z), as<float>(bias), as<int>(idx),
-                      (int)h->size(0), as<float>(h), ptr(o.t), c.stream()) == GSPN_OK);
+    RUN(ssm_step, &d, ptr(x), ptr(dt), as<float>(A), ptr(B), ptr(C), as<float>(D), ptr(z), as<float>(bias), as<int>(idx),
+                      (int)h->size(0), as<float>(h), ptr(o.t), c.stream());
     return o.object(a[10]);
 }
 
@@ -367,11 +388,11 @@ PyObject* norm_forward(PyObject*, PyObject* const* a, Py_ssize_t) {
     NEED(c.start(y));
     const ScalarType res = r ? r->scalar_type() : c.ty;
     gspn_norm_desc d;
-    NEED(norm_desc(c, y, gate, wp, bp, scale, r, w, b, res, a[10], PyObject_IsTrue(a[11]), d));
+    NEED(norm_desc(c, y, gate, wp, bp, scale, r, w, b, res, a[10], yes(a[11]), d));
     Out s, q;
     NEED(s.take(c, r_out, true, res, y->sizes()) && q.take(c, w ? o : nullptr, w, c.ty, y->sizes()));
-    NEED(lib.norm_forward(&d, ptr(y), ptr(gate), as<float>(wp), as<float>(bp), as<float>(scale), ptr(r), as<float>(w), as<float>(b),
-                          ptr(s.t), ptr(q.t), c.stream()) == GSPN_OK);
+    RUN(norm_forward, &d, ptr(y), ptr(gate), as<float>(wp), as<float>(bp), as<float>(scale), ptr(r), as<float>(w), as<float>(b),
+                          ptr(s.t), ptr(q.t), c.stream());
     return tuple({s.object(a[8]), q.object(a[9])});
 }
 
@@ -383,7 +404,7 @@ PyObject* norm_backward(PyObject*, PyObject* const* a, Py_ssize_t) {
     NEED(c.start(y) && (w != nullptr) == (go != nullptr) && (r || dr) && (r || !w));
     const ScalarType res = r ? r->scalar_type() : dr->scalar_type();
     gspn_norm_desc d;
-    NEED(norm_desc(c, y, gate, wp, bp, scale, r, w, b, res, a[10], PyObject_IsTrue(a[11]), d));
+    NEED(norm_desc(c, y, gate, wp, bp, scale, r, w, b, res, a[10], yes(a[11]), d));
     NEED(c.opt(dr, res, y->sizes()) && c.opt(go, c.ty, y->sizes()));
     const size_t bytes = lib.norm_ws(&d, 1);
     NEED(bytes > 0);
@@ -394,9 +415,9 @@ PyObject* norm_backward(PyObject*, PyObject* const* a, Py_ssize_t) {
     NEED(dy.take(c, nullptr, true, c.ty, y->sizes()) && dri.take(c, nullptr, true, res, y->sizes()) &&
          dg.take(c, nullptr, gate, c.ty, y->sizes()) && dwp.take(c, nullptr, wp, f, cs) && dbp.take(c, nullptr, bp, f, cs) &&
          ds.take(c, nullptr, scale, f, cs) && dw.take(c, nullptr, w, f, cs) && db.take(c, nullptr, b, f, cs));
-    NEED(lib.norm_backward(&d, ptr(y), ptr(gate), as<float>(wp), as<float>(bp), as<float>(scale), ptr(r), as<float>(w), ptr(dr),
+    RUN(norm_backward, &d, ptr(y), ptr(gate), as<float>(wp), as<float>(bp), as<float>(scale), ptr(r), as<float>(w), ptr(dr),
                            ptr(go), ptr(dy.t), ptr(dri.t), ptr(dg.t), as<float>(dwp.t), as<float>(dbp.t), as<float>(ds.t),
-                           as<float>(dw.t), as<float>(db.t), ws.data_ptr(), bytes, c.stream()) == GSPN_OK);
+                           as<float>(dw.t), as<float>(db.t), ws.data_ptr(), bytes, c.stream());
     return tuple({dy.object(nullptr), dri.object(nullptr), dg.object(nullptr), dwp.object(nullptr), dbp.object(nullptr),
                   ds.object(nullptr), dw.object(nullptr), db.object(nullptr)});
 }
@@ -409,6 +430,7 @@ PyObject* guarded(PyObject* self, PyObject* const* a, Py_ssize_t n) {
         PyErr_SetString(PyExc_TypeError, "wrong number of arguments");
         return nullptr;
     }
+    if (!PyBool_Check(a[ARGS - 1])) DECLINE;                      // other truths may fail to be one
     try {
         return F(self, a, n);
     } catch (...) {

@@ -180,3 +180,35 @@ def test_binding_refuses_wrong_tensors():
         with pytest.raises(kind):
             f()
             pytest.fail(f"call {k} was taken")
+
+
+@pytest.mark.gpu
+def test_an_error_of_the_device_is_raised_and_the_call_not_made_again():
+    """A step that reached the device with an error is not repeated by the path that explains refusals. The entry
+    point is a stand-in on the host that only counts."""
+    x, w, state = torch.ones(2, 64, device="cuda"), torch.ones(64, 4, device="cuda"), torch.zeros(2, 3, 64, device="cuda")
+    g.conv_step(x, w, None, state.clone())
+    fast = pytest.importorskip("linear_spatial_propagation_gspn_b200._seq_fast")
+    real = {n: ctypes.cast(getattr(g.lib(), n), ctypes.c_void_p).value for n in seq.SIGNATURES}
+    calls = []
+    fake = ctypes.CFUNCTYPE(ctypes.c_int, *[ctypes.c_void_p] * 5, ctypes.c_int, *[ctypes.c_void_p] * 3)(
+        lambda *a: calls.append(a) or g.GSPN_ERR_CUDA)
+    fast.init({**real, "gspn_conv_step": ctypes.cast(fake, ctypes.c_void_p).value})
+    try:
+        with pytest.raises(g.GspnError) as e:
+            g.conv_step(x, w, None, state)
+    finally:
+        fast.init(real)
+    assert e.value.status == g.GSPN_ERR_CUDA and len(calls) == 1 and not state.any()
+    g.conv_step(x, w, None, state)
+    assert torch.equal(state.sum(1), torch.ones(2, 64, device="cuda"))
+
+
+@pytest.mark.gpu
+def test_flags_that_are_no_truth():
+    x, w = torch.ones(2, 64, device="cuda"), torch.ones(64, 4, device="cuda")
+    state = torch.zeros(2, 3, 64, device="cuda")
+    with pytest.raises((RuntimeError, ValueError)):
+        g.conv_step(x, w, None, state, silu=torch.ones(3))
+    assert not state.any()
+    assert torch.equal(g.conv_step(x, w, None, state.clone(), silu=1), g.conv_step(x, w, None, state.clone(), silu=True))
