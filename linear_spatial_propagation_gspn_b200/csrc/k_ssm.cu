@@ -105,8 +105,9 @@ struct Place {
 // end, and begun last it ran on by itself (8192 x 2048, nine sequences, the longest of 2277 tokens the last one:
 // forward 198 -> 144 us, backward 661 -> 498). Every thread compares one with all the others, which is paid by
 // each block: with 128 sequences of 64 tokens 183 -> 242 us, so only up to kRanked, beyond which lengths even out.
+// Not inlined: the scan that follows was compiled 3 % slower with it in place.
 constexpr int kRanked = 32;
-__device__ __forceinline__ int nth_longest(const int* cu, int S, int n) {
+__device__ __noinline__ int nth_longest(const int* cu, int S, int n) {
     __shared__ int found;
     const int i = threadIdx.x;
     if (i < S) {
