@@ -257,3 +257,21 @@ def test_autograd(cu):
     # a broadcast gradient of the output, and no use of the state
     y = g.selective_scan(*(leaf[k].detach().requires_grad_(True) for k in names[:5]), cu=c)
     y.sum().backward()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("kind", ["rates", "steps"])
+def test_states_that_do_not_decay_stay_as_they_are(dtype, kind):
+    """A rate or a step of zero decays by one exactly, over any number of tokens: prompt, gradient and token."""
+    t = make(2, 500, 48, 1, 16, dtype, seed=11)
+    t["Bm"].zero_() if kind == "rates" else t["dt"].zero_()
+    A = torch.zeros_like(t["A"]) if kind == "rates" else t["A"]
+    kw = dict(D=t["D"], z=t["z"], h0=t["h0"], softplus=False)
+    h = torch.empty_like(t["h0"])
+    dt = t["dt"].abs()
+    y, save = g.ssm_forward_save(t["x"], dt, A, t["Bm"], t["Cm"], h=h, **kw)
+    assert torch.equal(h, t["h0"])
+    dh0 = g.ssm_backward(t["x"], dt, A, t["Bm"], t["Cm"], torch.zeros_like(y), save, dh=t["dh"], **kw)[-1]
+    assert torch.equal(dh0, t["dh"])
+    g.ssm_step(t["x"][:, 0], dt[:, 0], A, t["Bm"][:, 0], t["Cm"][:, 0], h, D=t["D"], z=t["z"][:, 0], softplus=False)
+    assert torch.equal(h, t["h0"])
