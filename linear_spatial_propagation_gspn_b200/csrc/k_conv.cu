@@ -6,7 +6,7 @@
 // with the K - 1 inputs before the present one in registers, so each input is loaded once per run; the
 // K - 1 tokens that neighbouring runs share come from the caches.
 //
-// Measured (B200, bf16, K = 4, silu): forward 8192 x 4096 33 us, 4.1 TB/s; 4 x 2048 x 2048 20 us, 3.3 TB/s;
+// Measured (B200, bf16, K = 4, silu): forward 8192 x 4096 31.5 us, 4.3 TB/s; 4 x 2048 x 2048 18.5 us, 3.6 TB/s;
 // backward of the latter 36 us, 2.8 TB/s, and 4.5 us for the sums of dw. A silu and its slope cost about as
 // many instruction slots (45 % taken) as the traffic costs time.
 #include "seq_common.cuh"
@@ -179,9 +179,10 @@ __device__ __forceinline__ void load_taps(const ConvArgs& p, int c, int n, f2 (&
 
 template <typename T, int K> __device__ void last_inputs(const ConvArgs& p, long long id);
 
-// Blocks behind the first `tokens` take the states behind the sequences.
+// Blocks behind the first `blocks` take the states behind the sequences. Seven blocks an SM by registers for
+// bf16 (32.9 -> 31.5 us at 8192 x 4096; eight spilled: 34.9), five for fp32 (seven spilled: 46 us against 27.5).
 template <typename T, int K, bool WIDE>
-__global__ void __launch_bounds__(128) k_conv_fwd(const ConvArgs p, long long blocks) {
+__global__ void __launch_bounds__(128, sizeof(T) == 2 ? 7 : 5) k_conv_fwd(const ConvArgs p, long long blocks) {
     constexpr int P = kVB / 2;
     constexpr int S = 4;
     __shared__ __align__(16) typename Raw<T, P>::type smem[WIDE ? S : 1][kBatch][128];
