@@ -1259,7 +1259,8 @@ bool fits(const SsmArgs& p) {
 // account, in units of one block's walk over a whole sequence. Blocks run in waves of one for each SM; two
 // forward blocks of up to 16 states fit one and then take 1.63 times as long (132 cycles a token, not 81). The
 // first pass over pieces costs 0.6 of the main one forward; backward a third, without waves, since its
-// blocks are small; joining them takes about 24 tokens' time for each piece, backward 12. Measured at 4096 tokens, bf16, N = 16 (us whole, then for these numbers of pieces):
+// blocks are small; joining them takes about 24 tokens' time for each piece, backward 12. Measured at
+// 4096 tokens, bf16, N = 16 (us whole, then for these numbers of pieces):
 //   forward    64 blocks 178, 4: 144, 10: 135    80 blocks 177, 3: 184, 10: 161   100 blocks 180, 2: 223, 8: 194
 //   backward   10 blocks 779, 6: 220, 12: 141    32 blocks 787, 4: 349, 12: 304    50 blocks 798, 2: 598, 8: 439
 // Forward a larger number has to gain 3 %, since the account is no better than that.
