@@ -49,7 +49,7 @@ struct Row {
     bool wide, edge;             // edge: a thread of the warp has columns outside the row
 };
 template <typename T, int E> struct Lay {
-    static constexpr int V = Vec<T>::V, H = E / 2, K = E / V;
+    static constexpr int V = Vec<T>::V, K = E / V;
     static __device__ __forceinline__ int col(const Row& w, int e) { return (e / V * w.tpr + w.tid) * V + e % V - w.phase; }
 };
 // A row's elements of type S as stored, V columns (16 or 32 bytes, or 8) at a time.
@@ -111,7 +111,6 @@ __device__ __forceinline__ void clear_row(RowRaw<T, S, E>& r, const Row& w) {
 }
 template <typename T, typename S, int E>
 __device__ __forceinline__ void open_row(const RowRaw<T, S, E>& r, f2 (&v)[E / 2]) {
-    constexpr int W = RowRaw<T, S, E>::W;
 #pragma unroll
     for (int h = 0; h < E / 2; ++h) {
         const int k = 2 * h / Vec<T>::V, at = 2 * h % Vec<T>::V;
@@ -122,7 +121,6 @@ __device__ __forceinline__ void open_row(const RowRaw<T, S, E>& r, f2 (&v)[E / 2
             v[h] = pack(__uint_as_float(q << 16), __uint_as_float(q & 0xffff0000u));
         }
     }
-    (void)W;
 }
 template <typename T, typename S, int E>
 __device__ __forceinline__ void st_row(S* p, const Row& w, const f2 (&v)[E / 2]) {
@@ -548,7 +546,7 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 && E == 8 ? 2 : 1) k_norm_bw
 // column instead, neighbouring threads on neighbouring columns. Parameters are read again for every row
 // and column sums wait in shared memory: neither fits the registers.
 template <typename T, int E, bool ALIGNED> struct WideLay {
-    static constexpr int V = Vec<T>::V, H = E / 2;
+    static constexpr int V = Vec<T>::V;
     static __device__ __forceinline__ int col(int e, int tid, int tpr) {
         return ALIGNED ? (e / V * tpr + tid) * V + e % V : e * tpr + tid;
     }
