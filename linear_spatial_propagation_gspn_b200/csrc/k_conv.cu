@@ -9,6 +9,7 @@
 // Measured (B200, bf16, K = 4, silu): forward 8192 x 4096 31.5 us, 4.3 TB/s; 4 x 2048 x 2048 18.5 us, 3.6 TB/s;
 // backward of the latter 36 us, 2.8 TB/s, and 4.5 us for the sums of dw. A silu and its slope cost about as
 // many instruction slots (45 % taken) as the traffic costs time.
+#include "conv_runs.h"
 #include "seq_common.cuh"
 
 namespace gspn {
@@ -19,13 +20,12 @@ constexpr int kRunFwd = 32, kRunBwd = 64;   // most tokens of a thread's run, fo
 constexpr int kBatch = 4;       // tokens taken together
 constexpr int kVB = 4;          // channels of a thread
 
-struct ConvArgs {
-    int B, L, C, S, silu;
+struct ConvArgs : Tokens {      // cu, L; S: sequences, packed or rows
+    int B, C, silu;
     bool wide, wide_w;          // 16-byte aligned vectors of channels; of filters
     const void* x;
     long long x_row, x_tok;
     const float *w, *bias;
-    const int* cu;
     const void *state0, *dy, *dstate;
     void *y, *state, *dx, *dstate0;
     float* part;
@@ -42,29 +42,6 @@ __device__ __forceinline__ void st_ch(T* p, const float (&v)[L], int n, bool wid
         for (int i = 0; i < L; ++i)
             if (i < n) Io<T>::st(p + i, v[i]);
     }
-}
-
-// The sequence of token t and its bounds; q = S and end = L where t lies behind the last one.
-struct Seq {
-    int q, start, end;
-};
-__device__ __forceinline__ int cu_at(const ConvArgs& p, int i) { return min(max(p.cu[i], 0), p.L); }
-__device__ __forceinline__ void enter(const ConvArgs& p, Seq& s, int t) {   // moves on to the sequence of t
-    while (s.q < p.S && t >= cu_at(p, s.q + 1)) ++s.q;
-    s.start = s.q < p.S ? min(cu_at(p, s.q), t) : t;
-    s.end = s.q < p.S ? cu_at(p, s.q + 1) : p.L;
-}
-__device__ __forceinline__ Seq find(const ConvArgs& p, int row, int t) {
-    if (!p.cu) return Seq{row, 0, p.L};
-    int lo = 0, hi = p.S;                        // first q with t < cu[q + 1]
-    while (lo < hi) {
-        const int mid = (lo + hi) / 2;
-        if (t < cu_at(p, mid + 1)) hi = mid;
-        else lo = mid + 1;
-    }
-    Seq s{lo, 0, 0};
-    enter(p, s, t);
-    return s;
 }
 
 // Loads of `P` pairs of channels (n of them exist): as stored, and taken apart.
@@ -115,7 +92,7 @@ template <typename T, int P, bool WIDE, int S> struct Ring {
         n = channels;
         put = got = 0;
     }
-    // Waits for the copies of batches that nobody takes: before a thread ends, or fills their places anew.
+    // Waits for the copies of batches that nobody takes, before their places are filled anew.
     __device__ __forceinline__ void leave() {
         if constexpr (WIDE) asm volatile("cp.async.wait_all;" ::: "memory");
     }
@@ -194,10 +171,9 @@ __global__ void __launch_bounds__(128, sizeof(T) == 2 ? 7 : 5) k_conv_fwd(const 
     const unsigned rr = id / (unsigned)p.nvec, cv = id - rr * p.nvec;
     const int row = (int)(rr / (unsigned)p.runs);
     if (row >= p.B) return;
-    int t = (int)(rr - row * (unsigned)p.runs) * p.run;
-    const int te = min(t + p.run, p.L);
-    const int c = (int)cv * kVB, n = p.C - c;
-    if (p.cu) t = max(t, cu_at(p, 0));
+    const Run r = run_at(p, (int)(rr - row * (unsigned)p.runs) * p.run, p.run);
+    int t = r.first;
+    const int te = r.end, c = (int)cv * kVB, n = p.C - c;
     if (t >= te) return;
     const T* xr = (const T*)p.x + row * p.x_row + c;
     T* yr = (T*)p.y + (long long)row * p.L * p.C + c;
@@ -229,7 +205,7 @@ __global__ void __launch_bounds__(128, sizeof(T) == 2 ? 7 : 5) k_conv_fwd(const 
     for (; t < te; t += kBatch) {
         ring.template take<1>(raw, te - t);
         ring.issue();
-        if (t + kBatch <= te && (!p.cu || (t + kBatch <= s.end && s.q < p.S))) {
+        if (t + kBatch <= te && (!p.cu || t + kBatch <= s.end)) {
 #pragma unroll
             for (int u = 0; u < kBatch; ++u) one(raw[u]);
         } else {
@@ -239,10 +215,6 @@ __global__ void __launch_bounds__(128, sizeof(T) == 2 ? 7 : 5) k_conv_fwd(const 
                 if (p.cu && t + u >= s.end) {
                     enter(p, s, t + u);
                     window<T, K, P>(p, xr, s, t + u, c, n, win);
-                }
-                if (p.cu && s.q >= p.S) {                         // behind the last sequence
-                    ring.leave();
-                    return;
                 }
                 one(raw[u]);
             }
@@ -304,16 +276,14 @@ __global__ void __launch_bounds__(128) k_conv_bwd(const ConvArgs p) {
         const long long all = (long long)p.B * p.runs;
         for (long long rr = (long long)blockIdx.y * kRows + grp; rr < all; rr += (long long)gridDim.y * kRows) {
             const int row = (int)(rr / p.runs);
-            int ta = (int)(rr % p.runs) * p.run;
-            const int tb = min(ta + p.run, p.L);
-            if (p.cu) ta = max(ta, cu_at(p, 0));
+            const Run run = run_at(p, (int)(rr % p.runs) * p.run, p.run);
+            const int ta = run.first, tb = run.end;
             if (ta >= tb) continue;
             const T* xr = (const T*)p.x + row * p.x_row + c;
             const T* gr = (const T*)p.dy + (long long)row * p.L * p.C + c;
             T* dr = (T*)p.dx + (long long)row * p.L * p.C + c;
             Seq s = find(p, row, ta);
-            if (p.cu && s.q >= p.S) continue;
-            const int stop = min(tb + K - 1, p.L);
+            const int stop = min(tb + K - 1, p.cu ? border(p, p.S) : p.L);
             R xs[kBatch], gs[kBatch];
             T* pd = dr + (long long)(ta - (K - 1)) * p.C;         // where token t - (K - 1) goes
             Ring<T, P, WIDE, S> rx, rg;
@@ -404,11 +374,8 @@ __global__ void __launch_bounds__(128) k_conv_bwd(const ConvArgs p) {
 #pragma unroll
                         for (int k = 0; k < K - 1; ++k) put(tt - (K - 1) + k, acc[k]);
                         open = tt < tb;
-                        if (open) {
-                            enter(p, s, tt);
-                            open = s.q < p.S;
-                        }
                         if (!open) break;
+                        enter(p, s, tt);
                         window<T, K, P>(p, xr, s, tt, c, n, win);
 #pragma unroll
                         for (int k = 0; k < K; ++k)
