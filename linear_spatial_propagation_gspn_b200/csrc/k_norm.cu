@@ -11,6 +11,7 @@
 // Measured (B200): forward 8192 x 4096, bf16 with an fp32 stream, gate and both norms, 82 us, 5.7 TB/s;
 // backward 193 us, 3.8 TB/s. 8190 x 1153, bf16, centred, all parts: 40 us forward (2.4 TB/s), 77 us backward
 // (2.0 TB/s), 37 and 72 us at 1152 columns.
+#include "norm_shape.h"
 #include "seq_common.cuh"
 
 namespace gspn {
@@ -143,7 +144,6 @@ __device__ __forceinline__ void st_row(S* p, const Row& w, const f2 (&v)[E / 2])
 
 // The parameters of a thread's columns, zero where it has none, wait in shared memory, each thread's apart:
 // shifted columns are not aligned in global memory.
-enum { kWPost, kBPost, kScale, kWPre, kBPre, kParams };
 template <typename T, int E> struct Params {
     float* at;                   // [parameter][E / 4][tpr][4]: neighbouring threads on neighbouring 16 bytes
     int stride;
@@ -306,6 +306,7 @@ template <typename T, typename R, int E, int MAXT, bool WARP = MAXT == 128>
 __global__ void __launch_bounds__(MAXT, MAXT == 128 ? 1 : E == 8 ? 4 : 2) k_norm_fwd(const NormArgs p) {
     constexpr int H = E / 2;
     __shared__ __align__(16) float buf[3][4][8];
+    static_assert(sizeof(buf) <= kStaticSmem, "over_48k counts it");
     extern __shared__ __align__(16) float smem[];
     RowSum<WARP> sum{buf};
     long long row, step;
@@ -407,6 +408,7 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 && E == 8 ? 2 : 1) k_norm_bw
     using Y = Lay<T, E>;
     constexpr int H = E / 2;
     __shared__ __align__(16) float buf[3][4][8];
+    static_assert(sizeof(buf) <= kStaticSmem, "over_48k counts it");
     extern __shared__ __align__(16) float smem[];
     RowSum<WARP> sum{buf};
     long long row, step;
@@ -662,6 +664,7 @@ template <typename T, typename R, int E, bool ALIGNED, int MAXT>
 __global__ void __launch_bounds__(MAXT, 1) k_norm_fwd_wide(const NormArgs p) {
     constexpr int H = E / 2;
     __shared__ float2 buf[3][32];
+    static_assert(sizeof(buf) <= kStaticSmem, "over_48k counts it");
     WideSum sum{buf};
     const int tid = threadIdx.x, tpr = blockDim.x;
     const long long row = blockIdx.x;
@@ -724,6 +727,7 @@ __global__ void __launch_bounds__(MAXT, 1) k_norm_bwd_wide(const NormArgs p) {
     using Y = WideLay<T, E, ALIGNED>;
     constexpr int H = E / 2;
     __shared__ float2 buf[3][32];
+    static_assert(sizeof(buf) <= kStaticSmem, "over_48k counts it");
     extern __shared__ __align__(16) unsigned char smem_raw[];
     WideSum sum{buf};
     const int tid = threadIdx.x, tpr = blockDim.x;
@@ -838,24 +842,6 @@ bool make_args(const gspn_norm_desc* d, NormArgs* p) {
     return true;
 }
 
-// How a row is held: elements of a thread, threads of a block (128 = four warps with a row each, `warp`), up to
-// seven places kept free for the phase; `wide`: the kernels for wide rows.
-struct Shape {
-    int e, threads;
-    bool warp, wide;
-};
-Shape shape_for(int C) {
-    const int n = C % 8 != 0 ? C + 7 : C;
-    if (n <= 256) return {8, 128, true, false};
-    if (n <= 2048) return {8, (n + 255) / 256 * 32, false, false};
-    if (n <= 4096) return {16, (n + 511) / 512 * 32, false, false};
-    return {16, (C + 511) / 512 * 32, false, true};
-}
-// Shared memory: parameters and the backward pass's column sums; of wide rows the latter only.
-size_t smem_for(const Shape& s, int slots) {
-    if (s.wide) return (size_t)slots * 8 * s.threads * sizeof(f2);
-    return (size_t)s.threads * s.e * (kParams + slots) * sizeof(float);
-}
 // Blocks: what fits the SMs at once by their registers (threads an SM: backward 512, 256 with 16 elements;
 // forward twice that), in whole periods of the phases, and no more than there are rows. Wide rows have
 // a block each, forward.
@@ -876,7 +862,7 @@ cudaError_t by_shape(const NormArgs& p, int blocks, cudaStream_t st) {
     const size_t smem = smem_for(s, FWD ? 0 : p.slots);
     auto go = [&](auto kernel) {
         cudaError_t e = cudaSuccess;
-        if (smem > 48 * 1024) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostSmem);
+        if (over_48k(smem)) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostSmem);
         if (e == cudaSuccess) kernel<<<blocks, s.threads, smem, st>>>(p);
         return e;
     };
