@@ -135,6 +135,11 @@ bool packed(const Ctx& c, Opt cu, const Tensor& x, int& S, int64_t& n) {
     S = (int)n;
     return true;
 }
+// Tells autograd that the call wrote to tensors of the caller's through their pointers.
+void wrote(std::initializer_list<Opt> ts) {
+    for (Opt t : ts)
+        if (t && !t->is_inference()) t->unsafeGetTensorImpl()->bump_version();
+}
 PyObject* wrap(Tensor t) { return THPVariable_Wrap(std::move(t)); }
 
 // A tensor to write to: the caller's, or a new one. `o` owns a new one.
@@ -191,6 +196,7 @@ PyObject* conv_forward(PyObject*, PyObject* const* a, Py_ssize_t) {
     NEED(o.take(c, y, true, c.ty, x->sizes()));
     RUN(conv_forward, &d, ptr(x), as<float>(w), as<float>(bias), as<int>(cu), ptr(state0), ptr(o.t), ptr(state),
                           c.stream());
+    wrote({y, state});
     return o.object(a[5]);
 }
 
@@ -236,6 +242,7 @@ PyObject* conv_step(PyObject*, PyObject* const* a, Py_ssize_t) {
     NEED(o.take(c, y, true, c.ty, x->sizes()));
     RUN(conv_step, &d, ptr(x), as<float>(w), as<float>(bias), as<int>(idx), (int)state->size(0), ptr(state), ptr(o.t),
                        c.stream());
+    wrote({state, y});
     return o.object(a[5]);
 }
 
@@ -284,6 +291,7 @@ PyObject* ssm_forward(PyObject*, PyObject* const* a, Py_ssize_t) {
     RUN(ssm_forward, &d, ptr(x), ptr(dt), as<float>(A), ptr(B), ptr(C), as<float>(D), ptr(z), as<float>(bias), as<int>(cu),
                          as<float>(h0), ptr(o.t), as<float>(h), save ? (float*)hsave.data_ptr() : nullptr,
                          bytes > 256 ? ws.data_ptr() : nullptr, bytes, c.stream());
+    wrote({y, h});
     if (!save) return o.object(a[10]);
     return tuple({o.object(a[10]), wrap(hsave)});
 }
@@ -343,6 +351,7 @@ PyObject* ssm_step(PyObject*, PyObject* const* a, Py_ssize_t) {
     NEED(o.take(c, y, true, c.ty, x->sizes()));
     RUN(ssm_step, &d, ptr(x), ptr(dt), as<float>(A), ptr(B), ptr(C), as<float>(D), ptr(z), as<float>(bias), as<int>(idx),
                       (int)h->size(0), as<float>(h), ptr(o.t), c.stream());
+    wrote({h, y});
     return o.object(a[10]);
 }
 
@@ -393,6 +402,7 @@ PyObject* norm_forward(PyObject*, PyObject* const* a, Py_ssize_t) {
     NEED(s.take(c, r_out, true, res, y->sizes()) && q.take(c, w ? o : nullptr, w, c.ty, y->sizes()));
     RUN(norm_forward, &d, ptr(y), ptr(gate), as<float>(wp), as<float>(bp), as<float>(scale), ptr(r), as<float>(w), as<float>(b),
                           ptr(s.t), ptr(q.t), c.stream());
+    wrote({r_out, w ? o : nullptr});
     return tuple({s.object(a[8]), q.object(a[9])});
 }
 

@@ -12,7 +12,8 @@ output that the caller passes, and hold nothing meaningful in one that is alloca
 autograd functions give zeros there).
 
 Every call runs on x's device, on ``stream`` (default: that device's current one), and what it
-allocates belongs to that stream.
+allocates belongs to that stream. A tensor of the caller's that a call writes to counts as changed in
+place: autograd refuses a backward pass that had kept it.
 """
 from __future__ import annotations
 
@@ -124,6 +125,14 @@ def _workspace(name, x, kind, values, backward):
 
 def _ptr(t):
     return None if t is None else t.data_ptr()
+
+
+def _wrote(*ts):
+    """Tells autograd that a call wrote to these tensors of the caller's (through their pointers, which it cannot
+    see): a graph that kept one of them for its backward pass then refuses it, as after any in-place operation."""
+    for t in ts:
+        if t is not None and not t.is_inference():
+            torch.autograd.graph.increment_version(t)
 
 
 def _on_device(fn):
@@ -248,9 +257,11 @@ def _conv_forward(x, w, bias, silu, cu, state0, y, state):
     dev, dt = x.device, x.dtype
     _opt("state0", state0, ss, dt, dev)
     _opt("state", state, ss, dt, dev)
+    given = y
     y = torch.empty(x.shape, dtype=dt, device=dev) if y is None else _is("y", y, x.shape, dt, dev)
     _ok(_fn("gspn_conv_forward")(_desc(ConvDesc, *values)[1], x.data_ptr(), w.data_ptr(), _ptr(bias), _ptr(cu), _ptr(state0),
                                  y.data_ptr(), _ptr(state), _stream(x)), "gspn_conv_forward")
+    _wrote(given, state)
     return y
 
 
@@ -271,6 +282,7 @@ def _conv_backward(x, w, bias, dy, silu, cu, state0, dstate, out):
     _is("dy", dy, x.shape, dt, dev)
     _opt("state0", state0, ss, dt, dev)
     _opt("dstate", dstate, ss, dt, dev)
+    given = out or ()
     if out is None:
         out = (torch.empty(x.shape, dtype=dt, device=dev), torch.empty_like(w), None if bias is None else torch.empty_like(bias),
                None if state0 is None else torch.empty_like(state0))
@@ -283,6 +295,7 @@ def _conv_backward(x, w, bias, dy, silu, cu, state0, dstate, out):
     _ok(_fn("gspn_conv_backward")(_desc(ConvDesc, *values)[1], x.data_ptr(), w.data_ptr(), _ptr(bias), _ptr(cu), _ptr(state0),
                                   dy.data_ptr(), _ptr(dstate), dx.data_ptr(), dw.data_ptr(), _ptr(db), _ptr(ds), _ptr(ws), n,
                                   _stream(x)), "gspn_conv_backward")
+    _wrote(*given)
     return dx, dw, db, ds
 
 
@@ -310,10 +323,12 @@ def _conv_step(x, w, bias, state, idx, silu, y):
     _is("state", state, (state.shape[0], K - 1, C), dt, dev)
     _slots(idx, state, B, dev)
     row, _ = _tokens("x", x, x.shape, dt, dev)
+    given = y
     y = torch.empty((B, C), dtype=dt, device=dev) if y is None else _is("y", y, (B, C), dt, dev)
     _ok(_fn("gspn_conv_step")(_desc(ConvDesc, B, 1, C, K, 0, _code(dt), int(bool(silu)), row, 0)[1], x.data_ptr(), w.data_ptr(),
                               _ptr(bias), _ptr(idx), state.shape[0], state.data_ptr(), y.data_ptr(), _stream(x)),
         "gspn_conv_step")
+    _wrote(state, given)
     return y
 
 
@@ -342,6 +357,7 @@ def _ssm_run(x, dt, A, Bm, Cm, D, z, dt_bias, softplus, cu, h0, y, h, save):
     dev = x.device
     _opt("h0", h0, ss, torch.float32, dev)
     _opt("h", h, ss, torch.float32, dev)
+    given = y
     y = torch.empty(x.shape, dtype=x.dtype, device=dev) if y is None else _is("y", y, x.shape, x.dtype, dev)
     hsave = None
     if save:
@@ -350,6 +366,7 @@ def _ssm_run(x, dt, A, Bm, Cm, D, z, dt_bias, softplus, cu, h0, y, h, save):
     _ok(_fn("gspn_ssm_forward")(_desc(SsmDesc, *values)[1], x.data_ptr(), dt.data_ptr(), A.data_ptr(), Bm.data_ptr(), Cm.data_ptr(),
                                 _ptr(D), _ptr(z), _ptr(dt_bias), _ptr(cu), _ptr(h0), y.data_ptr(), _ptr(h), _ptr(hsave), _ptr(ws),
                                 n, _stream(x)), "gspn_ssm_forward")
+    _wrote(given, h)
     return y, hsave
 
 
@@ -409,6 +426,7 @@ def _ssm_backward(x, dt, A, Bm, Cm, dy, hsave, D, z, dt_bias, softplus, cu, h0, 
     def like(t, shape, dtype):
         return None if t is None else torch.empty(shape, dtype=dtype, device=dev)
 
+    given = out or ()
     if out is None:
         out = (like(x, x.shape, ty), like(x, x.shape, ty), like(A, A.shape, f), like(Bm, Bm.shape, ty), like(Cm, Cm.shape, ty),
                like(D, (x.shape[2],), f), like(z, x.shape, ty), like(dt_bias, (x.shape[2],), f), like(h0, ss, f))
@@ -425,6 +443,7 @@ def _ssm_backward(x, dt, A, Bm, Cm, dy, hsave, D, z, dt_bias, softplus, cu, h0, 
                                  _ptr(D), _ptr(z), _ptr(dt_bias), _ptr(cu), hsave.data_ptr(), dy.data_ptr(), _ptr(dh),
                                  dx.data_ptr(), ddt.data_ptr(), dA.data_ptr(), dB.data_ptr(), dC.data_ptr(), _ptr(dD), _ptr(dz),
                                  _ptr(dbias), _ptr(dh0), ws.data_ptr(), n, _stream(x)), "gspn_ssm_backward")
+    _wrote(*given)
     return dx, ddt, dA, dB, dC, dD, dz, dbias, dh0
 
 
@@ -454,10 +473,12 @@ def _ssm_step(x, dt, A, Bm, Cm, h, D, z, dt_bias, softplus, idx, y):
     xr, dr = _tokens("x", x, x.shape, ty, dev)[0], _tokens("dt", dt, x.shape, ty, dev)[0]
     zr = 0 if z is None else _tokens("z", z, x.shape, ty, dev)[0]
     br, cr = (_tokens(n, t.unsqueeze(1), (B, 1, G, N), ty, dev)[0] for n, t in (("Bm", Bm), ("Cm", Cm)))
+    given = y
     y = torch.empty((B, C), dtype=ty, device=dev) if y is None else _is("y", y, (B, C), ty, dev)
     desc = _desc(SsmDesc, B, 1, C, G, N, 0, _code(ty), int(bool(softplus)), xr, 0, dr, 0, zr, 0, br, 0, cr, 0)[1]
     _ok(_fn("gspn_ssm_step")(desc, x.data_ptr(), dt.data_ptr(), A.data_ptr(), Bm.data_ptr(), Cm.data_ptr(), _ptr(D), _ptr(z),
                              _ptr(dt_bias), _ptr(idx), h.shape[0], h.data_ptr(), y.data_ptr(), _stream(x)), "gspn_ssm_step")
+    _wrote(h, given)
     return y
 
 
@@ -526,7 +547,7 @@ def norm_forward(y, r=None, gate=None, w_post=None, b_post=None, scale=None, w_p
 def _norm_forward(y, r, gate, w_post, b_post, scale, w_pre, b_pre, eps, center, r_out, o):
     rt = y.dtype if r is None else r.dtype
     values = _norm_args(y, gate, w_post, b_post, scale, r, w_pre, b_pre, eps, center, rt)
-    dev = y.device
+    dev, given = y.device, (r_out, o if w_pre is not None else None)
     r_out = torch.empty(y.shape, dtype=rt, device=dev) if r_out is None else _is("r_out", r_out, y.shape, rt, dev)
     if w_pre is None:
         o = None
@@ -534,6 +555,7 @@ def _norm_forward(y, r, gate, w_post, b_post, scale, w_pre, b_pre, eps, center, 
         o = torch.empty(y.shape, dtype=y.dtype, device=dev) if o is None else _is("o", o, y.shape, y.dtype, dev)
     _ok(_fn("gspn_norm_forward")(_desc(NormDesc, *values)[1], y.data_ptr(), _ptr(gate), _ptr(w_post), _ptr(b_post), _ptr(scale),
                                  _ptr(r), _ptr(w_pre), _ptr(b_pre), r_out.data_ptr(), _ptr(o), _stream(y)), "gspn_norm_forward")
+    _wrote(*given)
     return r_out, o
 
 

@@ -212,3 +212,69 @@ def test_flags_that_are_no_truth():
         g.conv_step(x, w, None, state, silu=torch.ones(3))
     assert not state.any()
     assert torch.equal(g.conv_step(x, w, None, state.clone(), silu=1), g.conv_step(x, w, None, state.clone(), silu=True))
+
+
+WRITES = ("conv_forward", "conv_backward", "conv_step", "ssm_forward", "ssm_forward_save", "ssm_backward", "ssm_step", "norm_forward")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("named", [False, True])
+@pytest.mark.parametrize("name", WRITES)
+def test_what_a_call_writes_is_known_to_autograd(name, named):
+    """Every tensor of the caller's that a call writes to counts as changed in place, on the path without the
+    interpreter and on the one that checks (a named stream); what it only reads does not."""
+    z = lambda *s: torch.ones(*s, device="cuda")  # noqa: E731
+    B, L, C, N = 2, 5, 8, 4
+    x, w, bias, A, D = z(B, L, C), z(C, 4), z(C), -z(C, N), z(C)
+    bc, state, h, v = z(B, L, 1, N), z(B, 3, C), z(B, C, N), z(B, L, C)
+    kw = dict(stream=torch.cuda.current_stream()) if named else {}
+    save = g.ssm_forward_save(x, x, A, bc, bc)[1]
+    out = [z(*t.shape) for t in ((x, w, bias, state) if name == "conv_backward" else (x, x, A, bc, bc, D, x, D, h))]
+    y, s1, h1, step = z(B, L, C), z(B, 3, C), z(B, C, N), z(B, C)
+    call, written = {
+        "conv_forward": (lambda: g.conv_forward(x, w, bias, state0=state, state=s1, y=y, **kw), [s1, y]),
+        "conv_backward": (lambda: g.conv_backward(x, w, bias, v, state0=state, out=out, **kw), out),
+        "conv_step": (lambda: g.conv_step(x[:, 0], w, bias, s1, y=step, **kw), [s1, step]),
+        "ssm_forward": (lambda: g.ssm_forward(x, x, A, bc, bc, D=D, z=v, h0=h, h=h1, y=y, **kw), [h1, y]),
+        "ssm_forward_save": (lambda: g.ssm_forward_save(x, x, A, bc, bc, D=D, z=v, h0=h, h=h1, y=y, **kw), [h1, y]),
+        "ssm_backward": (lambda: g.ssm_backward(x, x, A, bc, bc, v, save, D=D, z=v, dt_bias=D, h0=h, out=out, **kw), out),
+        "ssm_step": (lambda: g.ssm_step(x[:, 0], x[:, 0], A, bc[:, 0], bc[:, 0], h1, D=D, y=step, **kw), [h1, step]),
+        "norm_forward": (lambda: g.norm_forward(x, v, w_pre=D, r_out=y, o=out[0], **kw), [y, out[0]]),
+    }[name]
+    read = [t for t in (x, w, bias, A, D, bc, state, h, v, save)]
+    before = [t._version for t in written], [t._version for t in read]
+    call()
+    assert [t._version for t in written] == [n + 1 for n in before[0]]
+    assert [t._version for t in read] == before[1]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("named", [False, True])
+@pytest.mark.parametrize("op", ["conv", "scan"])
+def test_a_state_moved_on_before_its_gradient_is_refused(op, named):
+    """The differentiable calls keep the state that a sequence starts from; a step that moves it on in place before
+    the backward pass must not end in gradients of another state."""
+    B, L, C, N = 2, 6, 8, 4
+    x = torch.randn(B, L, C, device="cuda", requires_grad=True)
+    kw = dict(stream=torch.cuda.current_stream()) if named else {}
+    if op == "conv":
+        w, state = torch.randn(C, 4, device="cuda"), torch.randn(B, 3, C, device="cuda")
+        y = g.causal_conv(x, w, state0=state)
+        g.conv_step(x.detach()[:, 0], w, None, state, **kw)
+    else:
+        A, bc, state = -torch.rand(C, N, device="cuda"), torch.randn(B, L, 1, N, device="cuda"), torch.randn(B, C, N, device="cuda")
+        y = g.selective_scan(x, x, A, bc, bc, h0=state)
+        d = x.detach()
+        g.ssm_step(d[:, 0], d[:, 0], A, bc[:, 0], bc[:, 0], state, **kw)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y.sum().backward()
+
+
+@pytest.mark.gpu
+def test_states_of_inference_tensors_are_written():
+    """Tensors made in inference mode have no count of changes; calls write to them all the same."""
+    with torch.inference_mode():
+        x, w, state = torch.ones(2, 8, device="cuda"), torch.ones(8, 4, device="cuda"), torch.zeros(2, 3, 8, device="cuda")
+        for kw in ({}, dict(stream=torch.cuda.current_stream())):
+            g.conv_step(x, w, None, state, **kw)
+    assert torch.equal(state.sum(1), torch.full((2, 8), 2.0, device="cuda"))
