@@ -5,6 +5,7 @@ import glob
 import os
 import subprocess
 import sys
+import warnings
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -29,11 +30,16 @@ def headers():
                   + glob.glob(os.path.join(INCLUDE, "*.h")))
 
 
+def _older(target: str, sources) -> bool:
+    return not os.path.exists(target) or any(os.path.getmtime(f) > os.path.getmtime(target) for f in sources)
+
+
 def stale() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(BINDING):
-        return True
-    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
-    return any(os.path.getmtime(f) > t for f in sources() + headers() + [BINDING_SRC, __file__])
+    return _older(LIB, sources() + headers() + [__file__])
+
+
+def binding_stale() -> bool:
+    return _older(BINDING, headers() + [BINDING_SRC, __file__])
 
 
 def binding_command(out: str):
@@ -52,9 +58,45 @@ def binding_command(out: str):
             "-I", INCLUDE, BINDING_SRC, "-o", out, "-L", lib, "-ltorch_python", "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda"]
 
 
+def _start_binding(out: str):
+    try:
+        return subprocess.Popen(binding_command(out))
+    except OSError:                      # no such compiler
+        return None
+
+
+def _finish_binding(process, out: str):
+    """Without the binding every call goes through the checks in Python: the same results, some 20 us a call later.
+    An older one is taken away, since it may disagree with the library about what they pass each other."""
+    if process is not None and process.wait() == 0:
+        os.replace(out, BINDING)
+        return
+    for f in (out, BINDING):
+        if os.path.exists(f):
+            os.remove(f)
+    warnings.warn(f"{os.path.basename(BINDING)} was not built (a C++ compiler, Python's and torch's headers are needed): "
+                  "token-sequence calls take the slower path through Python", RuntimeWarning, stacklevel=3)
+
+
 def build(force: bool = False, verbose: bool = False, extra=()) -> str:
-    if not force and not stale():
-        return LIB
+    """Compiles libgspn.so, and the native binding of the token-sequence calls where that is possible."""
+    binding = None
+    if force or binding_stale():
+        tmp_binding = BINDING + f".tmp{os.getpid()}"
+        binding = (_start_binding(tmp_binding), tmp_binding)
+    if force or stale():
+        try:
+            _build_library(verbose, extra)
+        except BaseException:
+            if binding and binding[0]:
+                binding[0].kill()
+            raise
+    if binding:
+        _finish_binding(*binding)
+    return LIB
+
+
+def _build_library(verbose, extra):
     nvcc = os.environ.get("NVCC", "nvcc")
     objdir = os.path.join(HERE, "_build")
     os.makedirs(objdir, exist_ok=True)
@@ -67,16 +109,12 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
             print(" ".join(cmd), file=sys.stderr)
         procs.append((subprocess.Popen(cmd), src))
         objs.append(obj)
-    tmp_binding = BINDING + f".tmp{os.getpid()}"
-    procs.append((subprocess.Popen(binding_command(tmp_binding)), BINDING_SRC))
     for p, src in procs:
         if p.wait() != 0:
-            raise RuntimeError(f"the compiler failed on {src}")
+            raise RuntimeError(f"nvcc failed on {src}")
     tmp = LIB + f".tmp{os.getpid()}"
     subprocess.check_call([nvcc, "-shared", "-gencode", "arch=compute_100a,code=sm_100a", "-o", tmp, *objs])
     os.replace(tmp, LIB)
-    os.replace(tmp_binding, BINDING)
-    return LIB
 
 
 if __name__ == "__main__":
