@@ -77,14 +77,20 @@ __device__ __forceinline__ float2 softplus_of(float2 v) {
 }
 __device__ __forceinline__ float softplus_of(float v) { return softplus_of(make_float2(v, v)).x; }
 
-// A token's decay 2^(d A2), A2 = A log2(e). The approximate exponential comes out low, by 1e-8 to 5e-8 on
-// average where -16 < v < -2^-9: nothing for one token, but the states of a slow channel multiply hundreds
-// of decays, and dA then loses 1.8e-6 of its norm (577 tokens, rates 1 .. 24, steps 1e-3 .. 1e-1). The
-// product is rounded once with a constant that takes the middle of that range up again: 6e-7, for nothing.
-// 2^kTilt rounds to 1, so a step of zero still leaves its state as it was.
-constexpr float kTilt = 2.8e-8f;
-__device__ __forceinline__ f2 decay2(f2 d, f2 A2) { return ex2_2(fma2(d, A2, both(kTilt))); }
-__device__ __forceinline__ float decay(float d, float A2) { return ex2(fmaf(d, A2, kTilt)); }
+// A token's decay 2^(d A2), A2 = A log2(e). The approximate exponential comes out low on average, and the states
+// of a slow channel multiply as many decays as they remember tokens. Its mean relative error, in 1e-8, by -v:
+// 0.5 to 0.9 below 2^-9, 0.7 to 2.2 up to 2^-7, 2.5 from there to 1/2 (0.6 to 3.1 by octave halves), 5 above 1. An
+// addend to the exponent takes it up again, rounded once together with the product: `tilt_of` follows those
+// figures to within 0.2 below 2^-9, where memory is longest. One addend for all, of 2.8e-8, left +1.4 there.
+// It changes slowly with v, so a tile of tokens shares the one that its first token's step gives.
+// 2^tilt rounds to 1, so a step of zero still leaves its state as it was.
+__device__ __forceinline__ float tilt_of(float v) { return fmaf(2.05e-8f, __saturatef(fmaf(200.f, fabsf(v), -0.5f)), 0.95e-8f); }
+__device__ __forceinline__ f2 tilt_of(f2 v) {
+    const float2 s = unpack(v);
+    return pack(tilt_of(s.x), tilt_of(s.y));
+}
+__device__ __forceinline__ f2 decay2(f2 d, f2 A2, f2 tilt) { return ex2_2(fma2(d, A2, tilt)); }
+__device__ __forceinline__ float decay(float d, float A2, float tilt) { return ex2(fmaf(d, A2, tilt)); }
 
 // Tokens of a piece: equal pieces, whole runs of kSub tokens so that saved states fall on borders.
 __device__ __forceinline__ int piece_len(int len, int K) {
@@ -433,6 +439,7 @@ __global__ void __launch_bounds__(32 * NL + Feed<NL>::threads, NL == 4 ? 2 : 1) 
             }
         };
         fetch(0, 0);
+        const f2 t01 = tilt_of(mul2(dd[0][0], A01)), t23 = tilt_of(mul2(dd[0][0], A23));
 #pragma unroll
         for (int t = 0; t < kTile; t += 4) {
             const int w = t / 4 & 1;
@@ -446,7 +453,7 @@ __global__ void __launch_bounds__(32 * NL + Feed<NL>::threads, NL == 4 ? 2 : 1) 
                 float b[4], cc[4];
                 if constexpr (LOCAL) get_b(bc[w][u], b);
                 else get_bc(bc[w][u], b, cc);
-                const f2 a01 = decay2(dd[w][u], A01), a23 = decay2(dd[w][u], A23);
+                const f2 a01 = decay2(dd[w][u], A01, t01), a23 = decay2(dd[w][u], A23, t23);
                 h01 = fma2(a01, h01, mul2(dx[w][u], pack(b[0], b[1])));
                 h23 = fma2(a23, h23, mul2(dx[w][u], pack(b[2], b[3])));
                 if constexpr (LOCAL) {
@@ -557,15 +564,18 @@ __global__ void __launch_bounds__(32 * NL) k_ssm_bwd_local(const SsmArgs p) {
         for (int i = 0; i < 4; ++i) (&sC[0][0])[i * P::threads + threadIdx.x] = Io<T>::ld(&rC[i]);
         __syncthreads();
         if (t0 - kTile >= q.lo) load(t0 - kTile);
+        float tilt[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) tilt[j] = tilt_of(sdr[0][cl].x * A2[j]);
 #pragma unroll 8
         for (int t = kTile - 1; t >= 0; --t) {
             const float2 dr = sdr[t][cl];
             const float4 c4 = *(const float4*)&sC[t][n0];
             sum_d += dr.x;
-            ag[0] = decay(dr.x, A2[0]) * fmaf(c4.x, dr.y, ag[0]);
-            ag[1] = decay(dr.x, A2[1]) * fmaf(c4.y, dr.y, ag[1]);
-            ag[2] = decay(dr.x, A2[2]) * fmaf(c4.z, dr.y, ag[2]);
-            ag[3] = decay(dr.x, A2[3]) * fmaf(c4.w, dr.y, ag[3]);
+            ag[0] = decay(dr.x, A2[0], tilt[0]) * fmaf(c4.x, dr.y, ag[0]);
+            ag[1] = decay(dr.x, A2[1], tilt[1]) * fmaf(c4.y, dr.y, ag[1]);
+            ag[2] = decay(dr.x, A2[2], tilt[2]) * fmaf(c4.z, dr.y, ag[2]);
+            ag[3] = decay(dr.x, A2[3], tilt[3]) * fmaf(c4.w, dr.y, ag[3]);
         }
         __syncthreads();
     }
@@ -858,6 +868,13 @@ __global__ void __launch_bounds__(kScan + kFeedB, 1) k_ssm_bwd(const SsmArgs p) 
             hin[s][1] = pack(f[2], f[3]);
         }
         load_h(i - 1);
+        f2 tilt[2][2];
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            const f2 d = both(sm.dd[buf][0][PRow<NL>::at(cl[s])].x);
+            tilt[s][0] = tilt_of(mul2(d, A2[s][0]));
+            tilt[s][1] = tilt_of(mul2(d, A2[s][1]));
+        }
 #pragma unroll
         for (int t = 0; t < kTB; ++t) {
             f2 b01, b23;
@@ -866,8 +883,8 @@ __global__ void __launch_bounds__(kScan + kFeedB, 1) k_ssm_bwd(const SsmArgs p) 
             for (int s = 0; s < 2; ++s) {
                 f2 d, dx;
                 ld_pairs((const float*)&sm.dd[buf][t][PRow<NL>::at(cl[s])], d, dx);
-                h[t][s][0] = fma2(decay2(d, A2[s][0]), t ? h[t - 1][s][0] : hin[s][0], mul2(dx, b01));
-                h[t][s][1] = fma2(decay2(d, A2[s][1]), t ? h[t - 1][s][1] : hin[s][1], mul2(dx, b23));
+                h[t][s][0] = fma2(decay2(d, A2[s][0], tilt[s][0]), t ? h[t - 1][s][0] : hin[s][0], mul2(dx, b01));
+                h[t][s][1] = fma2(decay2(d, A2[s][1], tilt[s][1]), t ? h[t - 1][s][1] : hin[s][1], mul2(dx, b23));
             }
         }
         f2 dAs[2][2];                                             // sums of 16 tokens join the long sum as one
@@ -922,7 +939,7 @@ __global__ void __launch_bounds__(kScan + kFeedB, 1) k_ssm_bwd(const SsmArgs p) 
                     vB[m] = s ? fma2(g, dx, vB[m]) : mul2(g, dx);
                     y = m ? fma2(c2[m], ht, y) : mul2(c2[m], ht);
                     gb = m ? fma2(g, b2[m], gb) : mul2(g, b2[m]);
-                    ag[s][m] = mul2(decay2(d, A2[s][m]), g);
+                    ag[s][m] = mul2(decay2(d, A2[s][m], tilt[s][m]), g);
                     const f2 e = mul2(ag[s][m], hp);
                     dAs[s][m] = fma2(e, d, dAs[s][m]);
                     ea = m ? fma2(e, A2[s][m], ea) : mul2(e, A2[s][m]);
@@ -1149,8 +1166,8 @@ __global__ void __launch_bounds__(kStep) k_ssm_step(const SsmArgs p, const int* 
         for (int i = 0; i < I; ++i) {
             if (!same_group) states(g[i]);
             const f2 di = both(I == 1 ? d : __shfl_sync(all, d, base + i)), dxi = both(I == 1 ? dx : __shfl_sync(all, dx, base + i));
-            h[i][0] = fma2(decay2(di, A2[i][0]), h[i][0], mul2(dxi, bv[0]));
-            h[i][1] = fma2(decay2(di, A2[i][1]), h[i][1], mul2(dxi, bv[1]));
+            h[i][0] = fma2(decay2(di, A2[i][0], tilt_of(mul2(di, A2[i][0]))), h[i][0], mul2(dxi, bv[0]));
+            h[i][1] = fma2(decay2(di, A2[i][1], tilt_of(mul2(di, A2[i][1]))), h[i][1], mul2(dxi, bv[1]));
             const float2 s = unpack(fma2(h[i][0], cv[0], mul2(h[i][1], cv[1])));
             y[i] = s.x + s.y;
         }
