@@ -137,9 +137,9 @@ GSPN_API gspn_status gspn_norm_forward(const gspn_norm_desc *desc, const void *y
 /* Gradients of sum(dr r_out) + sum(go o), given r_out as the forward left it (r_row is its row
  * stride): dy, dr_in (the gradient of r, res_dtype), dgate, dw_post, db_post, dscale, dw_pre, db_pre.
  * dr (or null), go: rows x C contiguous, dr of res_dtype. go and r_out go with w_pre. Each output
- * may be null where its input is null; dr_in may be null. Rows over 4096 columns have their column sums in
- * shared memory: asked for more than 200 KB of them, the call returns GSPN_ERR_UNSUPPORTED (all five
- * fit up to 10240 columns, four up to 12800, three up to 16384). */
+ * but dy may be null, and has to be where its input is null (dr_in excepted). Rows over 4096 columns have their
+ * column sums in shared memory: asked for more than 200 KB of them, the call returns GSPN_ERR_UNSUPPORTED (all
+ * five fit up to 10240 columns, four up to 12800, three up to 16384; the others take a second call). */
 GSPN_API gspn_status gspn_norm_backward(const gspn_norm_desc *desc, const void *y, const void *gate,
                                         const float *w_post, const float *b_post, const float *scale,
                                         const void *r_out, const float *w_pre, const void *dr, const void *go,

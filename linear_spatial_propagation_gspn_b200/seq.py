@@ -591,9 +591,18 @@ def _norm_backward(y, r_out, dr, do, gate, w_post, b_post, scale, w_pre, b_pre, 
     sums = tuple(like(t) for t in (w_post, b_post, scale, w_pre, b_pre))
     n = _size("gspn_norm_workspace_size", dev.index, NormDesc, values, 1)
     ws = torch.empty(n, dtype=torch.uint8, device=dev)
-    _ok(_fn("gspn_norm_backward")(_desc(NormDesc, *values)[1], y.data_ptr(), _ptr(gate), _ptr(w_post), _ptr(b_post), _ptr(scale),
-                                  _ptr(r_out), _ptr(w_pre), _ptr(dr), _ptr(do), dy.data_ptr(), dr_in.data_ptr(), _ptr(dgate),
-                                  *map(_ptr, sums), ws.data_ptr(), n, _stream(y)), "gspn_norm_backward")
+
+    def run(*wanted):
+        return _fn("gspn_norm_backward")(_desc(NormDesc, *values)[1], y.data_ptr(), _ptr(gate), _ptr(w_post), _ptr(b_post), _ptr(scale),
+                                         _ptr(r_out), _ptr(w_pre), _ptr(dr), _ptr(do), dy.data_ptr(), dr_in.data_ptr(), _ptr(dgate),
+                                         *map(_ptr, wanted), ws.data_ptr(), n, _stream(y))
+
+    status = run(*sums)
+    if status == _pkg().GSPN_ERR_UNSUPPORTED and sum(t is not None for t in sums) > 3:
+        # Column sums of so wide rows fit three at a time: the other norm's in a second pass, which writes the rows'
+        # gradients again, the same ones.
+        status = run(*sums[:3], None, None) or run(None, None, None, *sums[3:])
+    _ok(status, "gspn_norm_backward")
     return (dy, dr_in, dgate, *sums)
 
 
