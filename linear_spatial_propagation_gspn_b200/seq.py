@@ -13,7 +13,8 @@ autograd functions give zeros there).
 
 Every call runs on x's device, on ``stream`` (default: that device's current one), and what it
 allocates belongs to that stream. A tensor of the caller's that a call writes to counts as changed in
-place: autograd refuses a backward pass that had kept it.
+place: autograd refuses a backward pass that had kept it. A batch of no rows is taken: nothing is launched, and
+gradients of parameters are zero.
 """
 from __future__ import annotations
 
@@ -157,6 +158,17 @@ def _on_device(fn):
     return call
 
 
+def _no_rows(x, *sums):
+    """True for a batch of no rows, which is no call of the library's: what it would add up (sums) is zero, and the
+    rest has no elements."""
+    if x.shape[0]:
+        return False
+    for t in sums:
+        if t is not None:
+            t.zero_()
+    return True
+
+
 def _stream(x):
     return torch.cuda.current_stream(x.device).cuda_stream
 
@@ -259,6 +271,8 @@ def _conv_forward(x, w, bias, silu, cu, state0, y, state):
     _opt("state", state, ss, dt, dev)
     given = y
     y = torch.empty(x.shape, dtype=dt, device=dev) if y is None else _is("y", y, x.shape, dt, dev)
+    if _no_rows(x):
+        return y
     _ok(_fn("gspn_conv_forward")(_desc(ConvDesc, *values)[1], x.data_ptr(), w.data_ptr(), _ptr(bias), _ptr(cu), _ptr(state0),
                                  y.data_ptr(), _ptr(state), _stream(x)), "gspn_conv_forward")
     _wrote(given, state)
@@ -291,6 +305,8 @@ def _conv_backward(x, w, bias, dy, silu, cu, state0, dstate, out):
     _is("dw", dw, w.shape, torch.float32, dev)
     _opt("dbias", db, (x.shape[2],), torch.float32, dev)
     _opt("dstate0", ds, ss, dt, dev)
+    if _no_rows(x, dw, db):
+        return dx, dw, db, ds
     ws, n = _workspace("gspn_conv_workspace_size", x, ConvDesc, values, 1)
     _ok(_fn("gspn_conv_backward")(_desc(ConvDesc, *values)[1], x.data_ptr(), w.data_ptr(), _ptr(bias), _ptr(cu), _ptr(state0),
                                   dy.data_ptr(), _ptr(dstate), dx.data_ptr(), dw.data_ptr(), _ptr(db), _ptr(ds), _ptr(ws), n,
@@ -325,6 +341,8 @@ def _conv_step(x, w, bias, state, idx, silu, y):
     row, _ = _tokens("x", x, x.shape, dt, dev)
     given = y
     y = torch.empty((B, C), dtype=dt, device=dev) if y is None else _is("y", y, (B, C), dt, dev)
+    if _no_rows(x):
+        return y
     _ok(_fn("gspn_conv_step")(_desc(ConvDesc, B, 1, C, K, 0, _code(dt), int(bool(silu)), row, 0)[1], x.data_ptr(), w.data_ptr(),
                               _ptr(bias), _ptr(idx), state.shape[0], state.data_ptr(), y.data_ptr(), _stream(x)),
         "gspn_conv_step")
@@ -359,6 +377,8 @@ def _ssm_run(x, dt, A, Bm, Cm, D, z, dt_bias, softplus, cu, h0, y, h, save):
     _opt("h", h, ss, torch.float32, dev)
     given = y
     y = torch.empty(x.shape, dtype=x.dtype, device=dev) if y is None else _is("y", y, x.shape, x.dtype, dev)
+    if _no_rows(x):
+        return y, torch.empty(0, dtype=torch.float32, device=dev) if save else None
     hsave = None
     if save:
         hsave = torch.empty(_size("gspn_ssm_hsave_size", dev.index, SsmDesc, values) // 4, dtype=torch.float32, device=dev)
@@ -419,7 +439,7 @@ def _ssm_backward(x, dt, A, Bm, Cm, dy, hsave, D, z, dt_bias, softplus, cu, h0, 
     values, ss = _ssm_args(x, dt, A, Bm, Cm, D, z, dt_bias, softplus, cu)
     dev, ty, f = x.device, x.dtype, torch.float32
     _is("dy", dy, x.shape, ty, dev)
-    _is("hsave", hsave, (_size("gspn_ssm_hsave_size", dev.index, SsmDesc, values) // 4,), f, dev)
+    _is("hsave", hsave, (_size("gspn_ssm_hsave_size", dev.index, SsmDesc, values) // 4 if x.shape[0] else 0,), f, dev)
     _opt("h0", h0, ss, f, dev)
     _opt("dh", dh, ss, f, dev)
 
@@ -437,6 +457,8 @@ def _ssm_backward(x, dt, A, Bm, Cm, dy, hsave, D, z, dt_bias, softplus, cu, h0, 
     _opt("dz", dz, x.shape, ty, dev)
     _opt("ddt_bias", dbias, (x.shape[2],), f, dev)
     _opt("dh0", dh0, ss, f, dev)
+    if _no_rows(x, dA, dD, dbias):
+        return dx, ddt, dA, dB, dC, dD, dz, dbias, dh0
     n = _size("gspn_ssm_workspace_size", dev.index, SsmDesc, values, 1)
     ws = torch.empty(n, dtype=torch.uint8, device=dev)
     _ok(_fn("gspn_ssm_backward")(_desc(SsmDesc, *values)[1], x.data_ptr(), dt.data_ptr(), A.data_ptr(), Bm.data_ptr(), Cm.data_ptr(),
@@ -475,6 +497,8 @@ def _ssm_step(x, dt, A, Bm, Cm, h, D, z, dt_bias, softplus, idx, y):
     br, cr = (_tokens(n, t.unsqueeze(1), (B, 1, G, N), ty, dev)[0] for n, t in (("Bm", Bm), ("Cm", Cm)))
     given = y
     y = torch.empty((B, C), dtype=ty, device=dev) if y is None else _is("y", y, (B, C), ty, dev)
+    if _no_rows(x):
+        return y
     desc = _desc(SsmDesc, B, 1, C, G, N, 0, _code(ty), int(bool(softplus)), xr, 0, dr, 0, zr, 0, br, 0, cr, 0)[1]
     _ok(_fn("gspn_ssm_step")(desc, x.data_ptr(), dt.data_ptr(), A.data_ptr(), Bm.data_ptr(), Cm.data_ptr(), _ptr(D), _ptr(z),
                              _ptr(dt_bias), _ptr(idx), h.shape[0], h.data_ptr(), y.data_ptr(), _stream(x)), "gspn_ssm_step")

@@ -278,3 +278,33 @@ def test_states_of_inference_tensors_are_written():
         for kw in ({}, dict(stream=torch.cuda.current_stream())):
             g.conv_step(x, w, None, state, **kw)
     assert torch.equal(state.sum(1), torch.full((2, 8), 2.0, device="cuda"))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_a_batch_of_no_rows(dtype):
+    """Prompts, gradients and tokens of no rows, as the norms take them: empty outputs, states as they were, zero
+    gradients of the parameters. Shapes are checked as ever."""
+    e = lambda *s: torch.empty(0, *s, dtype=dtype, device="cuda")  # noqa: E731
+    f = lambda *s: torch.ones(*s, device="cuda")  # noqa: E731
+    C, N, K = 8, 4, 4
+    x, bc, w, bias, A, s0, h0 = e(5, C), e(5, 1, N), f(C, K), f(C), -f(C, N), e(K - 1, C), f(0, C, N)
+    assert g.conv_forward(x, w, bias, state0=s0, state=s0).shape == x.shape
+    dx, dw, db, ds = g.conv_backward(x, w, bias, x, state0=s0)
+    assert dx.shape == x.shape and ds.shape == s0.shape and not dw.any() and not db.any() and dw.shape == w.shape
+    y, save = g.ssm_forward_save(x, x, A, bc, bc, D=bias, z=x, dt_bias=bias, h0=h0)
+    assert y.shape == g.ssm_forward(x, x, A, bc, bc).shape == x.shape
+    got = g.ssm_backward(x, x, A, bc, bc, x, save, D=bias, z=x, dt_bias=bias, h0=h0)
+    assert [t.shape for t in got] == [t.shape for t in (x, x, A, bc, bc, bias, x, bias, h0)]
+    assert not any(got[i].any() for i in (2, 5, 7))
+    pool, states, idx = f(3, K - 1, C).to(dtype), f(3, C, N), torch.empty(0, dtype=torch.int32, device="cuda")
+    for i in (None, idx):
+        assert g.conv_step(e(C), w, None, pool, idx=i).shape == g.ssm_step(e(C), e(C), A, e(1, N), e(1, N), states, idx=i).shape == (0, C)
+    assert (pool == 1).all() and (states == 1).all()
+    leaf = [t.clone().requires_grad_(True) for t in (x, w, A)]
+    (g.causal_conv(leaf[0], leaf[1]).sum() + g.selective_scan(leaf[0], x, leaf[2], bc, bc).sum()).backward()
+    assert not any(t.grad.any() for t in leaf)
+    with pytest.raises(ValueError):
+        g.conv_forward(x, f(C + 1, K))
+    with pytest.raises(ValueError):
+        g.ssm_backward(x, x, A, bc, bc, x, f(8))
