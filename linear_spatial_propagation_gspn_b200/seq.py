@@ -181,9 +181,20 @@ def _code(t):
     raise TypeError(f"unsupported dtype {t} (float32 or bfloat16)")
 
 
-def _is(name, t, shape, dtype, device, contiguous=True):
+def _tensor(name, t):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
+    return t
+
+
+def _axes(name, t, form, n):
+    if _tensor(name, t).dim() != n:
+        raise ValueError(f"{name} must be {form}")
+    return t.shape
+
+
+def _is(name, t, shape, dtype, device, contiguous=True):
+    _tensor(name, t)
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
     if t.dtype != dtype:
@@ -216,7 +227,7 @@ def _tokens(name, t, shape, dtype, device):
 def _packed(cu, x):
     if cu is None:
         return 0, x.shape[0]
-    if cu.dim() != 1 or cu.shape[0] < 2:
+    if _tensor("cu", cu).dim() != 1 or cu.shape[0] < 2:
         raise ValueError("cu must hold the S + 1 borders of the sequences")
     _is("cu", cu, cu.shape, torch.int32, x.device)
     if x.shape[0] != 1:
@@ -232,18 +243,10 @@ def _slots(idx, state, rows, device):
     return _is("idx", idx, (rows,), torch.int32, device)
 
 
-def _three(x, name="x"):
-    if x.dim() != 3:
-        raise ValueError(f"{name} must be (B, L, C)")
-    return x.shape
-
-
 # ------------------------------------------------------------------------------- convolution
 def _conv_args(x, w, bias, silu, cu):
-    B, L, C = _three(x)
-    if w.dim() != 2:
-        raise ValueError("w must be (C, K)")
-    K = w.shape[1]
+    B, L, C = _axes("x", x, "(B, L, C)", 3)
+    K = _axes("w", w, "(C, K)", 2)[1]
     dev = x.device
     _is("w", w, (C, K), torch.float32, dev)
     _opt("bias", bias, (C,), torch.float32, dev)
@@ -328,11 +331,8 @@ def conv_step(x, w, bias, state, idx=None, silu=True, y=None, stream=None):
 
 @_on_device
 def _conv_step(x, w, bias, state, idx, silu, y):
-    if x.dim() != 2:
-        raise ValueError("x must be (B, C)")
-    if w.dim() != 2:
-        raise ValueError("w must be (C, K)")
-    (B, C), K = x.shape, w.shape[1]
+    (B, C), K = _axes("x", x, "(B, C)", 2), _axes("w", w, "(C, K)", 2)[1]
+    _axes("state", state, "(slots, K-1, C)", 3)
     dev, dt = x.device, x.dtype
     _is("w", w, (C, K), torch.float32, dev)
     _opt("bias", bias, (C,), torch.float32, dev)
@@ -352,10 +352,8 @@ def _conv_step(x, w, bias, state, idx, silu, y):
 
 # ------------------------------------------------------------------------------ selective scan
 def _ssm_args(x, dt, A, Bm, Cm, D, z, dt_bias, softplus, cu):
-    B, L, C = _three(x)
-    if Bm.dim() != 4:
-        raise ValueError("Bm and Cm must be (B, L, G, N)")
-    G, N = Bm.shape[2:]
+    B, L, C = _axes("x", x, "(B, L, C)", 3)
+    G, N = _axes("Bm", Bm, "(B, L, G, N)", 4)[2:]
     dev, ty, f = x.device, x.dtype, torch.float32
     if G < 1 or C % G:
         raise ValueError(f"{G} groups do not divide {C} channels")
@@ -481,9 +479,8 @@ def ssm_step(x, dt, A, Bm, Cm, h, D=None, z=None, dt_bias=None, softplus=True, i
 
 @_on_device
 def _ssm_step(x, dt, A, Bm, Cm, h, D, z, dt_bias, softplus, idx, y):
-    if x.dim() != 2 or Bm.dim() != 3:
-        raise ValueError("x must be (B, C), Bm and Cm (B, G, N)")
-    (B, C), (G, N) = x.shape, Bm.shape[1:]
+    (B, C), (G, N) = _axes("x", x, "(B, C)", 2), _axes("Bm", Bm, "(B, G, N)", 3)[1:]
+    _axes("h", h, "(slots, C, N)", 3)
     dev, ty, f = x.device, x.dtype, torch.float32
     if G < 1 or C % G:
         raise ValueError(f"{G} groups do not divide {C} channels")
@@ -494,7 +491,7 @@ def _ssm_step(x, dt, A, Bm, Cm, h, D, z, dt_bias, softplus, idx, y):
     _slots(idx, h, B, dev)
     xr, dr = _tokens("x", x, x.shape, ty, dev)[0], _tokens("dt", dt, x.shape, ty, dev)[0]
     zr = 0 if z is None else _tokens("z", z, x.shape, ty, dev)[0]
-    br, cr = (_tokens(n, t.unsqueeze(1), (B, 1, G, N), ty, dev)[0] for n, t in (("Bm", Bm), ("Cm", Cm)))
+    br, cr = (_tokens(n, _tensor(n, t).unsqueeze(1), (B, 1, G, N), ty, dev)[0] for n, t in (("Bm", Bm), ("Cm", Cm)))
     given = y
     y = torch.empty((B, C), dtype=ty, device=dev) if y is None else _is("y", y, (B, C), ty, dev)
     if _no_rows(x):
@@ -509,9 +506,7 @@ def _ssm_step(x, dt, A, Bm, Cm, h, D, z, dt_bias, softplus, idx, y):
 # ------------------------------------------------------------------------- norms around a block
 def _rows(name, t, shape, dtypes, device):
     """Stride between the rows of a (..., C) tensor that is one run of rows."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.device != device:
+    if _tensor(name, t).device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
     if t.dtype not in dtypes:
         raise TypeError(f"{name} has dtype {t.dtype}, expected {' or '.join(map(str, dtypes))}")
@@ -569,7 +564,7 @@ def norm_forward(y, r=None, gate=None, w_post=None, b_post=None, scale=None, w_p
 
 @_on_device
 def _norm_forward(y, r, gate, w_post, b_post, scale, w_pre, b_pre, eps, center, r_out, o):
-    rt = y.dtype if r is None else r.dtype
+    rt = y.dtype if r is None else _tensor("r", r).dtype
     values = _norm_args(y, gate, w_post, b_post, scale, r, w_pre, b_pre, eps, center, rt)
     dev, given = y.device, (r_out, o if w_pre is not None else None)
     r_out = torch.empty(y.shape, dtype=rt, device=dev) if r_out is None else _is("r_out", r_out, y.shape, rt, dev)
@@ -601,7 +596,7 @@ def _norm_backward(y, r_out, dr, do, gate, w_post, b_post, scale, w_pre, b_pre, 
         raise ValueError("do goes with w_pre")
     if r_out is None and dr is None or r_out is None and w_pre is not None:
         raise ValueError("r_out (or, without w_pre, dr) must be given")
-    rt = (dr if r_out is None else r_out).dtype
+    rt = (_tensor("dr", dr) if r_out is None else _tensor("r_out", r_out)).dtype
     values = _norm_args(y, gate, w_post, b_post, scale, r_out, w_pre, b_pre, eps, center, rt)
     dev, ty = y.device, y.dtype
     _opt("dr", dr, y.shape, rt, dev)
@@ -639,8 +634,8 @@ def _fresh(t, cu):
 class _CausalConv(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, w, bias, silu, cu, state0, return_state):
-        S, n = _packed(cu, x) if x.dim() == 3 else (0, 0)
-        state = torch.empty((n, w.shape[1] - 1, x.shape[-1]), dtype=x.dtype, device=x.device) if return_state else None
+        S, n = _packed(cu, x) if _tensor("x", x).dim() == 3 else (0, 0)
+        state = torch.empty((n, _axes("w", w, "(C, K)", 2)[1] - 1, x.shape[-1]), dtype=x.dtype, device=x.device) if return_state else None
         y = conv_forward(x, w, bias, silu=silu, cu=cu, state0=state0, y=_fresh(x, cu), state=state)
         ctx.save_for_backward(x, w, bias, cu, state0)
         ctx.silu = silu
@@ -665,8 +660,8 @@ def causal_conv(x, w, bias=None, silu=True, cu=None, state0=None, return_state=F
 class _SelectiveScan(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, dt, A, Bm, Cm, D, z, dt_bias, softplus, cu, h0, return_state):
-        S, n = _packed(cu, x) if x.dim() == 3 else (0, 0)
-        h = torch.empty((n, *A.shape), dtype=torch.float32, device=x.device) if return_state else None
+        S, n = _packed(cu, x) if _tensor("x", x).dim() == 3 else (0, 0)
+        h = torch.empty((n, *_axes("A", A, "(C, N)", 2)), dtype=torch.float32, device=x.device) if return_state else None
         kw = dict(D=D, z=z, dt_bias=dt_bias, softplus=softplus, cu=cu, h0=h0, y=_fresh(x, cu), h=h)
         ctx.softplus = softplus
         if any(ctx.needs_input_grad):

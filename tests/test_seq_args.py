@@ -308,3 +308,28 @@ def test_a_batch_of_no_rows(dtype):
         g.conv_forward(x, f(C + 1, K))
     with pytest.raises(ValueError):
         g.ssm_backward(x, x, A, bc, bc, x, f(8))
+
+
+@pytest.mark.gpu
+def test_what_is_no_tensor_is_named():
+    """A list, a number or nothing where a tensor has to be: a TypeError that names the argument."""
+    z = lambda *s, **k: torch.zeros(*s, device="cuda", **k)  # noqa: E731
+    x, w, A, B, h, st = z(2, 4, 8), z(8, 4), z(8, 2), z(2, 4, 1, 2), z(2, 8, 2), z(2, 3, 8)
+    bad = [
+        ("w", lambda: g.conv_forward(x, None)), ("bias", lambda: g.conv_forward(x, w, 1.0)), ("cu", lambda: g.conv_forward(x[:1], w, cu=[0, 4])),
+        ("state0", lambda: g.conv_forward(x, w, state0=0)), ("dy", lambda: g.conv_backward(x, w, None, None)),
+        ("w", lambda: g.conv_step(x[:, 0], [1], None, st)), ("state", lambda: g.conv_step(x[:, 0], w, None, None)),
+        ("idx", lambda: g.conv_step(x[:, 0], w, None, st, idx=[0, 1])), ("Bm", lambda: g.ssm_forward(x, x, A, None, B)),
+        ("Cm", lambda: g.ssm_forward(x, x, A, B, None)), ("A", lambda: g.ssm_forward(x, x, 1, B, B)), ("dt", lambda: g.ssm_forward(x, None, A, B, B)),
+        ("hsave", lambda: g.ssm_backward(x, x, A, B, B, x, None)), ("h", lambda: g.ssm_step(x[:, 0], x[:, 0], A, B[:, 0], B[:, 0], None)),
+        ("Cm", lambda: g.ssm_step(x[:, 0], x[:, 0], A, B[:, 0], None, h)), ("r", lambda: g.norm_forward(x, 1)),
+        ("w_pre", lambda: g.norm_forward(x, x, w_pre=[1])), ("r_out", lambda: g.norm_backward(x, 2, None, x, w_pre=z(8))),
+        ("w", lambda: g.causal_conv(x, None, return_state=True)), ("A", lambda: g.selective_scan(x, x, None, B, B, return_state=True)),
+        ("x", lambda: g.causal_conv(None, w)), ("x", lambda: g.selective_scan(None, x, A, B, B)),
+    ]
+    for name, f in bad:
+        with pytest.raises(TypeError, match=f"^{name} must be a torch.Tensor"):
+            f()
+    for f in (lambda: g.conv_step(x[:, 0], w, None, st[0]), lambda: g.ssm_step(x[:, 0], x[:, 0], A, B[:, 0], B[:, 0], h[0])):
+        with pytest.raises(ValueError):
+            f()
