@@ -659,12 +659,12 @@ def causal_conv(x, w, bias=None, silu=True, cu=None, state0=None, return_state=F
 
 class _SelectiveScan(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, x, dt, A, Bm, Cm, D, z, dt_bias, softplus, cu, h0, return_state):
+    def forward(ctx, x, dt, A, Bm, Cm, D, z, dt_bias, softplus, cu, h0, return_state, grad):
         S, n = _packed(cu, x) if _tensor("x", x).dim() == 3 else (0, 0)
         h = torch.empty((n, *_axes("A", A, "(C, N)", 2)), dtype=torch.float32, device=x.device) if return_state else None
         kw = dict(D=D, z=z, dt_bias=dt_bias, softplus=softplus, cu=cu, h0=h0, y=_fresh(x, cu), h=h)
         ctx.softplus = softplus
-        if any(ctx.needs_input_grad):
+        if grad and any(ctx.needs_input_grad):
             y, hsave = ssm_forward_save(x, dt, A, Bm, Cm, **kw)
             ctx.save_for_backward(x, dt, A, Bm, Cm, D, z, dt_bias, cu, h0, hsave)
         else:
@@ -679,12 +679,13 @@ class _SelectiveScan(torch.autograd.Function):
         out = (_fresh(x, cu), _fresh(x, cu), like(A), _fresh(Bm, cu), _fresh(Cm, cu), like(D), _fresh(z, cu), like(dt_bias), like(h0))
         g = ssm_backward(x, dt, A, Bm, Cm, dy.contiguous(), hsave, D=D, z=z, dt_bias=dt_bias, softplus=ctx.softplus, cu=cu,
                          h0=h0, dh=None if dh is None else dh.contiguous(), out=out)
-        return (*g[:8], None, None, g[8], None)
+        return (*g[:8], None, None, g[8], None, None)
 
 
 def selective_scan(x, dt, A, Bm, Cm, D=None, z=None, dt_bias=None, softplus=True, cu=None, h0=None, return_state=False):
     """Differentiable ssm_forward; with return_state, (y, h)."""
-    return _SelectiveScan.apply(x, dt, A, Bm, Cm, D, z, dt_bias, softplus, cu, h0, return_state)
+    # needs_input_grad tells what the inputs ask for, under no_grad too
+    return _SelectiveScan.apply(x, dt, A, Bm, Cm, D, z, dt_bias, softplus, cu, h0, return_state, torch.is_grad_enabled())
 
 
 class _BlockNorm(torch.autograd.Function):

@@ -83,3 +83,17 @@ def test_norms_of_outputs(N, G):
         if not off(v, ref[name]) <= 2 * one:
             bad[name] = off(v, ref[name]) / one
     assert not bad, bad
+
+
+def test_no_states_are_kept_without_gradients(monkeypatch):
+    """Under no_grad the differentiable call is the plain one, though its parameters ask for gradients."""
+    from linear_spatial_propagation_gspn_b200 import seq
+
+    x, bc = torch.randn(2, 40, 32, device="cuda"), torch.randn(2, 40, 1, 16, device="cuda")
+    A = (-torch.rand(32, 16, device="cuda")).requires_grad_(True)
+    want = g.selective_scan(x, x, A, bc, bc)
+    assert want.requires_grad
+    monkeypatch.setattr(seq, "ssm_forward_save", lambda *a, **k: pytest.fail("states were kept"))
+    with torch.no_grad():
+        got = g.selective_scan(x, x, A, bc, bc)
+    assert torch.equal(got, want) and not got.requires_grad
