@@ -276,9 +276,11 @@ __global__ void __launch_bounds__(128) k_conv_bwd(const ConvArgs p) {
         const long long all = (long long)p.B * p.runs;
         for (long long rr = (long long)blockIdx.y * kRows + grp; rr < all; rr += (long long)gridDim.y * kRows) {
             const int row = (int)(rr / p.runs);
-            const Run run = run_at(p, (int)(rr % p.runs) * p.run, p.run);
-            const int ta = run.first, tb = run.end;
-            if (ta >= tb) continue;
+            // tb: where the next run begins (not run.end, which could not be formed anew and made the compiler spill)
+            const int at = (int)(rr % p.runs) * p.run, tb = min(at + p.run, p.L);
+            const Run run = run_at(p, at, p.run);
+            const int ta = run.first;
+            if (ta >= run.end) continue;
             const T* xr = (const T*)p.x + row * p.x_row + c;
             const T* gr = (const T*)p.dy + (long long)row * p.L * p.C + c;
             T* dr = (T*)p.dx + (long long)row * p.L * p.C + c;
@@ -373,8 +375,10 @@ __global__ void __launch_bounds__(128) k_conv_bwd(const ConvArgs p) {
                     if (tt >= s.end) {                            // the sequence is over: its last sums are complete
 #pragma unroll
                         for (int k = 0; k < K - 1; ++k) put(tt - (K - 1) + k, acc[k]);
-                        open = tt < tb;
-                        if (!open) break;
+                        if (tt >= tb) {
+                            open = false;
+                            break;
+                        }
                         enter(p, s, tt);
                         window<T, K, P>(p, xr, s, tt, c, n, win);
 #pragma unroll
