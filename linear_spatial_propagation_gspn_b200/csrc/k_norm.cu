@@ -53,7 +53,7 @@ template <typename T, int E> struct Lay {
     static constexpr int V = Vec<T>::V, K = E / V;
     static __device__ __forceinline__ int col(const Row& w, int e) { return (e / V * w.tpr + w.tid) * V + e % V - w.phase; }
 };
-// A row's elements of type S as stored, V columns (16 or 32 bytes, or 8) at a time.
+// A row's elements of type S as stored, V columns (16 or 32 bytes) at a time.
 template <typename T, typename S, int E> struct RowRaw {
     static constexpr int W = Vec<T>::V * sizeof(S) / 4;           // words of a vector
     uint32_t q[E / Vec<T>::V][W];
@@ -72,15 +72,10 @@ __device__ __forceinline__ void ld_row(RowRaw<T, S, E>& r, const S* p, const Row
         const int c = Y::col(w, k * V);
         if (c >= w.C) continue;
         if (w.wide && (more || c + V <= w.C)) {
-            if constexpr (W == 2) {
-                const uint2 v = *(const uint2*)(p + c);
-                r.q[k][0] = v.x; r.q[k][1] = v.y;
-            } else {
 #pragma unroll
-                for (int m = 0; m < W; m += 4) {
-                    const uint4 v = *((const uint4*)(p + c) + m / 4);
-                    r.q[k][m] = v.x; r.q[k][m + 1] = v.y; r.q[k][m + 2] = v.z; r.q[k][m + 3] = v.w;
-                }
+            for (int m = 0; m < W; m += 4) {
+                const uint4 v = *((const uint4*)(p + c) + m / 4);
+                r.q[k][m] = v.x; r.q[k][m + 1] = v.y; r.q[k][m + 2] = v.z; r.q[k][m + 3] = v.w;
             }
         } else {
 #pragma unroll
@@ -564,14 +559,9 @@ __device__ __forceinline__ void wide_ld_row(const S* p, int C, int tid, int tpr,
         for (int k = 0; k < E / V; ++k) {
             const int c = Y::col(k * V, tid, tpr);
 #pragma unroll
-            for (int m = 0; m < V; m += (Q < V ? Q : V)) {
-                if constexpr (Q <= V) {
-                    const uint4 q = c < C ? *(const uint4*)(p + c + m) : make_uint4(0, 0, 0, 0);
-                    to_pairs(q, *(f2(*)[Q / 2])(v + (k * V + m) / 2));
-                } else {
-                    const uint2 q = c < C ? *(const uint2*)(p + c) : make_uint2(0, 0);
-                    to_pairs(q, *(f2(*)[2])(v + k * V / 2));
-                }
+            for (int m = 0; m < V; m += Q) {
+                const uint4 q = c < C ? *(const uint4*)(p + c + m) : make_uint4(0, 0, 0, 0);
+                to_pairs(q, *(f2(*)[Q / 2])(v + (k * V + m) / 2));
             }
         }
     } else {
