@@ -82,12 +82,15 @@ __device__ __forceinline__ float softplus_of(float v) { return softplus_of(make_
 // 0.5 to 0.9 below 2^-9, 0.7 to 2.2 up to 2^-7, 2.5 from there to 1/2 (0.6 to 3.1 by octave halves), 5 above 1. An
 // addend to the exponent takes it up again, rounded once together with the product: `tilt_of` follows those
 // figures to within 0.2 below 2^-9, where memory is longest. One addend for all, of 2.8e-8, left +1.4 there.
-// It changes slowly with v, so a tile of tokens shares the one that its first token's step gives.
+// It changes slowly with v, so a tile of tokens shares that of one step: forward of the token ahead of it (which is
+// known before the tile begins: 16384 x 4096 703 us, against 713 with the tile's own first one), backward of its own
+// first token (445 us for 4 x 2048 x 2048; renewed at the end of the tile before, the registers ran out: 456).
 // 2^tilt rounds to 1, so a step of zero still leaves its state as it was.
-__device__ __forceinline__ float tilt_of(float v) { return fmaf(2.05e-8f, __saturatef(fmaf(200.f, fabsf(v), -0.5f)), 0.95e-8f); }
+__device__ __forceinline__ float tilt_step(float v) { return __saturatef(fmaf(200.f, fabsf(v), -0.5f)); }
+__device__ __forceinline__ float tilt_of(float v) { return fmaf(2.05e-8f, tilt_step(v), 0.95e-8f); }
 __device__ __forceinline__ f2 tilt_of(f2 v) {
     const float2 s = unpack(v);
-    return pack(tilt_of(s.x), tilt_of(s.y));
+    return fma2(pack(tilt_step(s.x), tilt_step(s.y)), both(2.05e-8f), both(0.95e-8f));
 }
 __device__ __forceinline__ f2 decay2(f2 d, f2 A2, f2 tilt) { return ex2_2(fma2(d, A2, tilt)); }
 __device__ __forceinline__ float decay(float d, float A2, float tilt) { return ex2(fmaf(d, A2, tilt)); }
@@ -425,6 +428,12 @@ __global__ void __launch_bounds__(32 * NL + Feed<NL>::threads, NL == 4 ? 2 : 1) 
     const long long save0 = LOCAL ? 0 : save_slot(p, q.sp, q.s);
     float sum_d = 0.f;
     __syncthreads();
+    f2 t01 = 0, t23 = 0;                                          // see tilt_of
+    if (tiles > 0) {
+        const f2 d = both(sm.dd[0][0][DRow::at(cl)].x);
+        t01 = tilt_of(mul2(d, A01));
+        t23 = tilt_of(mul2(d, A23));
+    }
     for (int i = 0; i < tiles; ++i) {
         const int t0 = q.lo + i * kTile, buf = i & 1;
         // Operands of four tokens are fetched while the four before are worked on; the stores below would
@@ -439,7 +448,6 @@ __global__ void __launch_bounds__(32 * NL + Feed<NL>::threads, NL == 4 ? 2 : 1) 
             }
         };
         fetch(0, 0);
-        const f2 t01 = tilt_of(mul2(dd[0][0], A01)), t23 = tilt_of(mul2(dd[0][0], A23));
 #pragma unroll
         for (int t = 0; t < kTile; t += 4) {
             const int w = t / 4 & 1;
@@ -462,6 +470,10 @@ __global__ void __launch_bounds__(32 * NL + Feed<NL>::threads, NL == 4 ? 2 : 1) 
                     const float2 s = unpack(fma2(h01, pack(cc[0], cc[1]), mul2(h23, pack(cc[2], cc[3]))));
                     sm.y[buf][t + u][YRow<NL>::at(cl, nl)] = s.x + s.y;
                 }
+            }
+            if (t + 4 == kTile) {
+                t01 = tilt_of(mul2(dd[w][3], A01));
+                t23 = tilt_of(mul2(dd[w][3], A23));
             }
         }
         __syncthreads();
@@ -782,7 +794,9 @@ __global__ void __launch_bounds__(kScan + kFeedB, 1) k_ssm_bwd(const SsmArgs p) 
                 for (int m = 0; m < 4; ++m) k0[m] = k1[m];
             }
             __syncthreads();
-            finish(i);                                            // d of tile i is overwritten behind the next barrier only
+            // The shares and sums of tile i are written again behind the next barrier only. Its d is not: the next
+            // stage() overwrites it before that, but each thread reads back only the entries that it staged itself.
+            finish(i);
         }
         // dD and d dt_bias: the threads that share a vector of channels, in order
         asm volatile("bar.sync 1, 256;" ::: "memory");
