@@ -6,7 +6,7 @@
 // with the K - 1 inputs before the present one in registers, so each input is loaded once per run; the
 // K - 1 tokens that neighbouring runs share come from the caches.
 //
-// Measured (B200, bf16, K = 4, silu): forward 8192 x 4096 31.5 us, 4.3 TB/s; 4 x 2048 x 2048 18.5 us, 3.6 TB/s;
+// Measured (B200, bf16, K = 4, silu): forward 8192 x 4096 30.8 us, 4.4 TB/s; 4 x 2048 x 2048 18 us, 3.7 TB/s;
 // backward of the latter 36 us, 2.8 TB/s, and 4.5 us for the sums of dw. A silu and its slope cost about as
 // many instruction slots (45 % taken) as the traffic costs time.
 #include "conv_runs.h"

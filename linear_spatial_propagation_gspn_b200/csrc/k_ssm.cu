@@ -17,10 +17,10 @@
 // pass joins the pieces before its own. That makes every exponential twice.
 //
 // Measured (B200, bf16, N = 16, gate, D and bias), against the exponentials' time alone:
-//   forward, 4 x 2048 tokens of 2048 channels, states saved   160 us   59 us   (two blocks an SM: 68 % of issue slots)
-//   the same backward                                         437 us   59 us   (54 % of issue slots, one block an SM)
-//   forward, one sequence of 16384 tokens, 4096 channels      686 us  236 us   (128 blocks, 81 cycles a token)
-//   a token of 256 rows of 4096 channels                       34 us   4.2 TB/s of states, A and inputs
+//   forward, 4 x 2048 tokens of 2048 channels, states saved   156 us   59 us   (two blocks an SM: 68 % of issue slots)
+//   the same backward, sums included                          448 us   59 us   (54 % of issue slots, one block an SM)
+//   forward, one sequence of 16384 tokens, 4096 channels      705 us  236 us   (128 blocks, 82 cycles a token)
+//   a token of 256 rows of 4096 channels                       36 us   4.0 TB/s of states, A and inputs
 // Issue slots and, with one block an SM, the scanning warp's latencies stand before the exponentials: a
 // token costs a block 200 instructions forward, of which the four scanning warps take about half.
 #include "seq_common.cuh"
@@ -82,9 +82,10 @@ __device__ __forceinline__ float softplus_of(float v) { return softplus_of(make_
 // 0.5 to 0.9 below 2^-9, 0.7 to 2.2 up to 2^-7, 2.5 from there to 1/2 (0.6 to 3.1 by octave halves), 5 above 1. An
 // addend to the exponent takes it up again, rounded once together with the product: `tilt_of` follows those
 // figures to within 0.2 below 2^-9, where memory is longest. One addend for all, of 2.8e-8, left +1.4 there.
-// It changes slowly with v, so a tile of tokens shares that of one step: forward of the token ahead of it (which is
-// known before the tile begins: 16384 x 4096 703 us, against 713 with the tile's own first one), backward of its own
-// first token (445 us for 4 x 2048 x 2048; renewed at the end of the tile before, the registers ran out: 456).
+// It changes slowly with v, so a tile of tokens shares that of one step: forward of the token ahead of it, which is
+// known before the tile begins (16384 x 4096: the addend costs 1.7 % of the pass, 2.0 with the tile's own first
+// token); backward of its own first token (4 x 2048 x 2048: 2 %; renewed at the end of the tile before, registers
+// ran out: 4 %). Single tokens have each their own (256 rows of 4096 channels: 34.0 -> 35.4 us).
 // 2^tilt rounds to 1, so a step of zero still leaves its state as it was.
 __device__ __forceinline__ float tilt_step(float v) { return __saturatef(fmaf(200.f, fabsf(v), -0.5f)); }
 __device__ __forceinline__ float tilt_of(float v) { return fmaf(2.05e-8f, tilt_step(v), 0.95e-8f); }
