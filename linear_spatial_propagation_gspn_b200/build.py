@@ -90,6 +90,9 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
         except BaseException:
             if binding and binding[0]:
                 binding[0].kill()
+                binding[0].wait()
+                if os.path.exists(binding[1]):
+                    os.remove(binding[1])
             raise
     if binding:
         _finish_binding(*binding)

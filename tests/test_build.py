@@ -38,11 +38,14 @@ def test_the_library_needs_nvcc_alone(small, monkeypatch, compiler):
 
 
 def test_a_library_that_does_not_compile_is_an_error(small, monkeypatch):
-    monkeypatch.setenv("CXX", "true")
+    script = small / "cxx"                                          # one that leaves its output behind and goes on
+    script.write_text('#!/bin/sh\nwhile [ "$1" != -o ]; do shift; done; : > "$2"; exec sleep 60\n')
+    script.chmod(0o755)
+    monkeypatch.setenv("CXX", str(script))
     (small / "one.cu").write_text("int one( {\n")
     with pytest.raises(RuntimeError, match="one.cu"):
         b.build(force=True)
-    assert not os.path.exists(b.LIB)
+    assert not any(f.endswith(".so") or ".tmp" in f for f in os.listdir(small))
 
 
 def test_calls_without_the_binding_take_the_checked_path(monkeypatch):
